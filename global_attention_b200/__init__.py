@@ -31,6 +31,16 @@ class ZgcmError(RuntimeError):
         self.status = status
 
 
+class _Rows(ctypes.Structure):   # zgcm_rows
+    _fields_ = [("ptr", ctypes.c_void_p), ("t_stride", ctypes.c_longlong), ("h_stride", ctypes.c_longlong)]
+
+
+class _Kv8Struct(ctypes.Structure):   # zgcm_kv8_cache
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scale", "v_scale", "k_mean", "k_tail",
+                                                "v_tail", "table")] +
+                [(n, ctypes.c_int) for n in ("n_seq", "n_blocks", "n_pages", "Hkv", "D", "code_type", "key_type")])
+
+
 def load() -> ctypes.CDLL:
     """Load libzgcm_attn.so (raises if it has not been built)."""
     global _lib
@@ -99,6 +109,23 @@ def load() -> ctypes.CDLL:
         lib.zgcm_proj_out_fwd.restype = i
         lib.zgcm_proj_out_bwd.argtypes = [vp, vp, vp, i, i, i, vp, vp, vp]
         lib.zgcm_proj_out_bwd.restype = i
+        sz, rows, cache = ctypes.c_size_t, _Rows, ctypes.POINTER(_Kv8Struct)
+        lib.zgcm_qk_norm_rope_fwd.argtypes = [rows, rows, vp, vp, vp] + [i] * 7 + [d, f, rows, rows, vp]
+        lib.zgcm_qk_norm_rope_fwd.restype = i
+        lib.zgcm_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+        lib.zgcm_qk_norm_rope_bwd_workspace_size.restype = sz
+        lib.zgcm_qk_norm_rope_bwd.argtypes = ([rows, rows, vp, vp, vp, rows, rows] + [i] * 7 +
+                                              [d, f, rows, rows, vp, vp, vp, sz, vp])
+        lib.zgcm_qk_norm_rope_bwd.restype = i
+        ll = ctypes.c_longlong
+        lib.zgcm_kv8_append.argtypes = [cache, vp, ll, ll, ll, vp, ll, ll, ll, vp, vp, i, vp]
+        lib.zgcm_kv8_append.restype = i
+        lib.zgcm_attn_decode_kv8_workspace_size.argtypes = [i, i, i]
+        lib.zgcm_attn_decode_kv8_workspace_size.restype = sz
+        lib.zgcm_attn_decode_kv8.argtypes = [cache, vp, vp, vp, vp, i, i, i, f, vp, vp, vp, sz, vp]
+        lib.zgcm_attn_decode_kv8.restype = i
+        lib.zgcm_kv8_select.argtypes = [cache, vp, vp, i, i, i, i, i, vp, vp]
+        lib.zgcm_kv8_select.restype = i
         _lib = lib
     return _lib
 
@@ -640,3 +667,334 @@ def zgcm_proj_out_bwd(a, w_o, dy, *, da=None, dw=None, stream=None):
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_proj_out_bwd")
     return da, dw
+
+
+# ------------------------------------- q/k normalisation and rotation (zgcm_qkrope.h)
+
+def _type_code(t, name):
+    import torch
+    for code, dtype in enumerate((torch.bfloat16, torch.float16, torch.float32)):
+        if t == dtype:
+            return code
+    raise TypeError(f"{name} must be bfloat16, float16 or float32")
+
+
+def _rows(t, name, dtype, shape):
+    """t: a [T, H, D] tensor of `dtype` whose rows of D are contiguous; its zgcm_rows.  Strides
+    of a dimension of one are not looked at (torch lets them be anything)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise TypeError(f"{name} must be a {dtype} tensor of rank 3 whose last dimension is contiguous")
+    if tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _out_rows(t, name, dtype, shape):
+    """_rows of an output: no two of its elements in one place."""
+    r = _rows(t, name, dtype, shape)
+    (T, H, D) = shape
+    dims = sorted((s, n) for s, n in ((r.t_stride, T), (r.h_stride, H)) if n > 1)
+    reach = D
+    for s, n in dims:
+        if s < reach:
+            raise TypeError(f"{name} must not overlap itself")
+        reach = s * (n - 1) + reach
+    return r
+
+
+class _on:
+    """Makes t's device the current one for the launches inside, where it is not already."""
+
+    def __init__(self, t):
+        import torch
+        index = t.device.index
+        self.guard = None if index is None or index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _qk_check(q, k, gamma_q, gamma_k, pos):
+    import torch
+    for n, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise TypeError(f"{n} must be a tensor of rank 3")
+    (T, Hq, D), Hkv = q.shape, k.shape[1]
+    code = _type_code(q.dtype, "q")
+    rq, rk = _rows(q, "q", q.dtype, (T, Hq, D)), _rows(k, "k", q.dtype, (T, Hkv, D))
+    _need(gamma_q, "gamma_q", torch.float32, (D,))
+    _need(gamma_k, "gamma_k", torch.float32, (D,))
+    _need(pos, "pos", torch.int32, (T,))
+    return T, Hq, Hkv, D, code, rq, rk
+
+
+def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_base=10000.0, eps=1e-6, out_dtype=None,
+                          qr=None, kr=None, stream=None):
+    """RMSNorm of every head's row, times gamma, rotated at the token's position: q [T,Hq,D], k [T,Hkv,D]
+    (bf16, fp16 or fp32, rows contiguous, any token and head strides that are multiples of 8), pos int32
+    [T].  Returns (qr, kr) of out_dtype (default: q's), or writes the tensors given."""
+    import torch
+    T, Hq, Hkv, D, xt, rq, rk = _qk_check(q, k, gamma_q, gamma_k, pos)
+    given = next((t for t in (qr, kr) if t is not None), None)
+    if out_dtype is None:
+        out_dtype = q.dtype if given is None else given.dtype
+    yt = _type_code(out_dtype, "out_dtype")
+    if given is not None:
+        for n, t, H in (("qr", qr, Hq), ("kr", kr, Hkv)):
+            if t is not None:
+                _out_rows(t, n, out_dtype, (T, H, D))
+    _one_device(("q", q), ("k", k), ("gamma_q", gamma_q), ("gamma_k", gamma_k), ("pos", pos), ("qr", qr), ("kr", kr))
+    if qr is None:
+        qr = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+    if kr is None:
+        kr = torch.empty((T, Hkv, D), dtype=out_dtype, device=q.device)
+    with _on(q):
+        st = load().zgcm_qk_norm_rope_fwd(rq, rk, _ptr(gamma_q), _ptr(gamma_k), _ptr(pos), T, Hq, Hkv, D, xt, yt,
+                                          int(rope_dims), float(rope_base), float(eps),
+                                          _rows(qr, "qr", out_dtype, (T, Hq, D)),
+                                          _rows(kr, "kr", out_dtype, (T, Hkv, D)), _stream(stream))
+    if st != ZGCM_OK:
+        raise ZgcmError(st, "zgcm_qk_norm_rope_fwd")
+    return qr, kr
+
+
+def zgcm_qk_norm_rope_bwd_workspace_size(T) -> int:
+    """Bytes of workspace zgcm_qk_norm_rope_bwd needs for T tokens."""
+    return int(load().zgcm_qk_norm_rope_bwd_workspace_size(int(T)))
+
+
+def zgcm_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, dqr, dkr, *, rope_dims=42, rope_base=10000.0, eps=1e-6,
+                          grads=None, workspace=None, stream=None):
+    """Gradients of zgcm_qk_norm_rope_fwd: dict dq, dk (q's dtype), dgamma_q, dgamma_k (fp32 [D], overwritten).
+    `grads` may supply them, `workspace` a uint8 tensor of zgcm_qk_norm_rope_bwd_workspace_size(T) bytes."""
+    import torch
+    T, Hq, Hkv, D, xt, rq, rk = _qk_check(q, k, gamma_q, gamma_k, pos)
+    if not isinstance(dqr, torch.Tensor):
+        raise TypeError("dqr must be a torch tensor")
+    yt = _type_code(dqr.dtype, "dqr")
+    rdq, rdk = _rows(dqr, "dqr", dqr.dtype, (T, Hq, D)), _rows(dkr, "dkr", dqr.dtype, (T, Hkv, D))
+    gl = []
+    if grads is not None:
+        _out_rows(grads["dq"], "dq", q.dtype, (T, Hq, D))
+        _out_rows(grads["dk"], "dk", q.dtype, (T, Hkv, D))
+        _need(grads["dgamma_q"], "dgamma_q", torch.float32, (D,))
+        _need(grads["dgamma_k"], "dgamma_k", torch.float32, (D,))
+        gl = [(n, grads[n]) for n in ("dq", "dk", "dgamma_q", "dgamma_k")]
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, 1, cuda=False)
+    _one_device(("q", q), ("k", k), ("gamma_q", gamma_q), ("gamma_k", gamma_k), ("pos", pos), ("dqr", dqr),
+                ("dkr", dkr), *gl, ("workspace", workspace))
+    if grads is None:
+        grads = dict(dq=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
+                     dk=torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device),
+                     dgamma_q=torch.empty(D, dtype=torch.float32, device=q.device),
+                     dgamma_k=torch.empty(D, dtype=torch.float32, device=q.device))
+    if workspace is None:
+        workspace = torch.empty(max(16, zgcm_qk_norm_rope_bwd_workspace_size(T)), dtype=torch.uint8, device=q.device)
+    with _on(q):
+        st = load().zgcm_qk_norm_rope_bwd(rq, rk, _ptr(gamma_q), _ptr(gamma_k), _ptr(pos), rdq, rdk, T, Hq, Hkv, D, xt,
+                                          yt, int(rope_dims), float(rope_base), float(eps),
+                                          _rows(grads["dq"], "dq", q.dtype, (T, Hq, D)),
+                                          _rows(grads["dk"], "dk", q.dtype, (T, Hkv, D)), _ptr(grads["dgamma_q"]),
+                                          _ptr(grads["dgamma_k"]), _ptr(workspace), workspace.numel(), _stream(stream))
+    if st != ZGCM_OK:
+        raise ZgcmError(st, "zgcm_qk_norm_rope_bwd")
+    return grads
+
+
+# ------------------------------------------------- 8-bit block cache (zgcm_kv8.h)
+
+KV8_BLOCK = 64
+
+
+def _window(w):
+    return min(int(w), 2 ** 31 - 1)   # a C int: any window this long reaches everything
+
+
+class ZgcmKv8Cache:
+    """A KV cache in 8-bit blocks of 64 tokens (include/zgcm_kv8.h): the tensors, checked once.
+
+    k_codes, v_codes [n_pages, Hkv, 64, D] float8_e4m3fn or int8; k_scale, v_scale [n_pages, Hkv] fp32;
+    k_mean [n_pages, Hkv, D] and k_tail [n_seq, Hkv, 64, D] bf16 or fp16 (the keys' type); v_tail
+    [n_seq, Hkv, 64, D] bf16; table [n_seq, n_blocks] int32, block j of a sequence in page
+    table[b][j mod n_blocks].  The tensors stay the caller's: pages are handed out by writing
+    numbers into `table` in place."""
+
+    _NAMES = ("k_codes", "v_codes", "k_scale", "v_scale", "k_mean", "k_tail", "v_tail", "table")
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, k_mean, k_tail, v_tail, table):
+        import torch
+        for n, t, ok in (("k_codes", k_codes, (torch.float8_e4m3fn, torch.int8)),
+                         ("k_tail", k_tail, (torch.bfloat16, torch.float16))):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype not in ok:
+                raise TypeError(f"{n} must be a tensor of rank 4 and one of {ok}")
+        P, Hkv, _, D = k_codes.shape
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise TypeError("table must be a tensor of rank 2")
+        n_seq, n_blocks = table.shape
+        _need(k_codes, "k_codes", k_codes.dtype, (P, Hkv, KV8_BLOCK, D))
+        _need(v_codes, "v_codes", k_codes.dtype, (P, Hkv, KV8_BLOCK, D))
+        _need(k_scale, "k_scale", torch.float32, (P, Hkv))
+        _need(v_scale, "v_scale", torch.float32, (P, Hkv))
+        _need(k_mean, "k_mean", k_tail.dtype, (P, Hkv, D))
+        _need(k_tail, "k_tail", k_tail.dtype, (n_seq, Hkv, KV8_BLOCK, D))
+        _need(v_tail, "v_tail", torch.bfloat16, (n_seq, Hkv, KV8_BLOCK, D))
+        _need(table, "table", torch.int32, (n_seq, n_blocks))
+        tensors = (k_codes, v_codes, k_scale, v_scale, k_mean, k_tail, v_tail, table)
+        _one_device(*zip(self._NAMES, tensors))
+        self._t = dict(zip(self._NAMES, tensors))
+        self.n_seq, self.n_blocks, self.n_pages, self.Hkv, self.D = n_seq, n_blocks, P, Hkv, D
+        self.key_dtype, self.device = k_tail.dtype, k_codes.device
+        self._c = _Kv8Struct(*(t.data_ptr() for t in tensors), n_seq, n_blocks, P, Hkv, D,
+                             0 if k_codes.dtype == torch.float8_e4m3fn else 1, 0 if k_tail.dtype == torch.bfloat16 else 1)
+        self._ref = ctypes.byref(self._c)
+
+    def __getattr__(self, name):
+        t = self.__dict__.get("_t", {})
+        if name in t:
+            return t[name]
+        raise AttributeError(name)
+
+    def __setattr__(self, name, value):
+        if name in self._NAMES:
+            raise AttributeError(f"{name} belongs to the cache: write into it (copy_), or make another cache")
+        object.__setattr__(self, name, value)
+
+
+def zgcm_kv8_alloc(n_seq, n_blocks, Hkv, *, n_pages=None, D=128, code_dtype=None, key_dtype=None, device="cuda"):
+    """A new ZgcmKv8Cache.  Without n_pages every sequence owns its n_blocks pages (table filled in order);
+    with it the table starts at -1 and the caller hands pages out."""
+    import torch
+    code_dtype = torch.float8_e4m3fn if code_dtype is None else code_dtype
+    key_dtype = torch.bfloat16 if key_dtype is None else key_dtype
+    if code_dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise TypeError("code_dtype must be float8_e4m3fn or int8")
+    if key_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("key_dtype must be bfloat16 or float16")
+    if n_pages is None:
+        n_pages = max(1, n_seq * n_blocks)
+        table = torch.arange(n_seq * n_blocks, dtype=torch.int32, device=device).view(n_seq, n_blocks)
+    else:
+        table = torch.full((n_seq, n_blocks), -1, dtype=torch.int32, device=device)
+    pages, tails = (n_pages, Hkv, KV8_BLOCK, D), (n_seq, Hkv, KV8_BLOCK, D)
+    codes = [torch.zeros(pages, dtype=torch.uint8, device=device).view(code_dtype) for _ in range(2)]
+    scales = [torch.zeros(pages[:2], dtype=torch.float32, device=device) for _ in range(2)]
+    return ZgcmKv8Cache(*codes, *scales, torch.zeros((n_pages, Hkv, D), dtype=key_dtype, device=device),
+                        torch.zeros(tails, dtype=key_dtype, device=device),
+                        torch.zeros(tails, dtype=torch.bfloat16, device=device), table)
+
+
+def _kv8_need(cache, *named):
+    """(name, tensor or None, dtype, shape): contiguous, of that shape, on the cache's device."""
+    if not isinstance(cache, ZgcmKv8Cache):
+        raise TypeError("cache must be a ZgcmKv8Cache")
+    for n, t, dtype, shape in named:
+        if t is not None:
+            _need(t, n, dtype, shape)
+            if t.device != cache.device:
+                raise TypeError(f"{n} must be on the cache's device ({cache.device}, a CUDA device)")
+
+
+def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
+    """Append tokens: k (cache.key_dtype, prepared: zgcm_qk_norm_rope_fwd) and v (bf16) [n_seq, N, Hkv, D], rows
+    contiguous, other strides multiples of 8; pos int32 [n_seq], the first token's position (negative: the sequence
+    is idle); count int32 [n_seq], the tokens of each sequence (default N).  Updates the cache in place."""
+    import torch
+    _kv8_need(cache)
+    for n, t, dtype in (("k", k, cache.key_dtype), ("v", v, torch.bfloat16)):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise TypeError(f"{n} must be a {dtype} tensor of rank 4 whose last dimension is contiguous")
+        if t.shape != (cache.n_seq, k.shape[1], cache.Hkv, cache.D):
+            raise TypeError(f"{n} must have shape {(cache.n_seq, k.shape[1], cache.Hkv, cache.D)}, not {tuple(t.shape)}")
+        if t.device != cache.device:
+            raise TypeError(f"{n} must be on the cache's device ({cache.device}, a CUDA device)")
+    _kv8_need(cache, ("pos", pos, torch.int32, (cache.n_seq,)), ("count", count, torch.int32, (cache.n_seq,)))
+    if not k.is_cuda:
+        raise TypeError("k must be a CUDA tensor")
+    ks, vs = ([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k, v))
+    with _on(k):
+        st = load().zgcm_kv8_append(cache._ref, _ptr(k), *ks, _ptr(v), *vs, _ptr(pos), _ptr(count), k.shape[1],
+                                    _stream(stream))
+    if st != ZGCM_OK:
+        raise ZgcmError(st, "zgcm_kv8_append")
+    return cache
+
+
+def zgcm_attn_decode_kv8_workspace_size(n_seq, Hq, Hkv) -> int:
+    """Bytes of workspace zgcm_attn_decode_kv8 needs."""
+    return int(load().zgcm_attn_decode_kv8_workspace_size(int(n_seq), int(Hq), int(Hkv)))
+
+
+def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=None, out=None, lse=None, workspace=None,
+                         stream=None):
+    """Decode attention of one token per sequence, appended before: q [n_seq,Hq,D] (cache.key_dtype, prepared),
+    g bf16 [n_seq,Hq,D] or None (no gate), pos int32 [n_seq].  blocks: int32 [n_seq,Hkv,n] from zgcm_kv8_select, the
+    earlier blocks to read (default: all that the window reaches).  Returns (out bf16 [n_seq,Hq,D], lse fp32 [n_seq,Hq])."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a tensor of rank 3")
+    _kv8_need(cache)
+    B, Hq, D = cache.n_seq, q.shape[1], cache.D
+    n_list = 0
+    if blocks is not None:
+        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3:
+            raise TypeError("blocks must be a tensor of rank 3")
+        n_list = blocks.shape[2]
+    _kv8_need(cache, ("q", q, cache.key_dtype, (B, Hq, D)), ("g", g, torch.bfloat16, (B, Hq, D)),
+              ("pos", pos, torch.int32, (B,)), ("blocks", blocks, torch.int32, (B, cache.Hkv, n_list)),
+              ("out", out, torch.bfloat16, (B, Hq, D)), ("lse", lse, torch.float32, (B, Hq)))
+    if not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(16, zgcm_attn_decode_kv8_workspace_size(B, Hq, cache.Hkv)), dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _check(workspace, "workspace", torch.uint8, 1, cuda=False)
+        if workspace.device != cache.device:
+            raise TypeError(f"workspace must be on the cache's device ({cache.device}, a CUDA device)")
+    if blocks is not None and n_list == 0:
+        blocks = pos   # an empty list: only whether there is one counts
+    with _on(q):
+        st = load().zgcm_attn_decode_kv8(cache._ref, _ptr(q), _ptr(g), _ptr(pos), _ptr(blocks), n_list, Hq, _window(window),
+                                         float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                         _stream(stream))
+    if st != ZGCM_OK:
+        raise ZgcmError(st, "zgcm_attn_decode_kv8")
+    return out, lse
+
+
+def zgcm_kv8_select(cache, q, pos, n_select, *, n_first=1, n_last=1, window=128, out=None, stream=None):
+    """The blocks a decode step should read: int32 [n_seq, Hkv, n_select], ascending, -1 behind the last, for
+    zgcm_attn_decode_kv8(blocks=...).  q [n_seq,Hq,D] (cache.key_dtype, prepared); a block's score is the largest
+    q . (mean of its keys) over the KV head's queries; the first n_first and last n_last candidates always count."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a tensor of rank 3")
+    _kv8_need(cache)
+    B, n_select = cache.n_seq, int(n_select)
+    _kv8_need(cache, ("q", q, cache.key_dtype, (B, q.shape[1], cache.D)), ("pos", pos, torch.int32, (B,)),
+              ("out", out, torch.int32, (B, cache.Hkv, n_select)))
+    if not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if out is None:
+        out = torch.empty((B, cache.Hkv, max(0, n_select)), dtype=torch.int32, device=q.device)
+    with _on(q):
+        st = load().zgcm_kv8_select(cache._ref, _ptr(q), _ptr(pos), q.shape[1], _window(window), n_select, int(n_first),
+                                    int(n_last), _ptr(out), _stream(stream))
+    if st != ZGCM_OK:
+        raise ZgcmError(st, "zgcm_kv8_select")
+    return out
