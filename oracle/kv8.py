@@ -52,12 +52,13 @@ def stored(x, code):
 def attend(q, g, k, v, *, code, window, scale=None, blocks=None):
     """The newest token's attention: q, g [Hq, D] (g may be None), k, v [S, Hkv, D] its
     sequence's tokens.  blocks: per KV head the earlier blocks to read.  Returns out [Hq, D], lse [Hq]
-    and the sums of |p v| (for tolerances) [Hq, D]."""
+    and, for tolerances, the sums of |p v| [Hq, D] and the sums over blocks of their largest p times
+    their largest |v| [Hq]."""
     q, kk, vv = _f64(q), stored(k, code), stored(v, code)
     S, Hkv, D = kk.shape
     scale = D ** -0.5 if scale is None else scale
     p = S - 1
-    out, lse, mag = np.zeros(q.shape), np.zeros(len(q)), np.zeros(q.shape)
+    out, lse, mag, top = np.zeros(q.shape), np.zeros(len(q)), np.zeros(q.shape), np.zeros(len(q))
     for h in range(len(q)):
         kv = h // (len(q) // Hkv)
         seen = np.arange(S) > p - window
@@ -71,10 +72,12 @@ def attend(q, g, k, v, *, code, window, scale=None, blocks=None):
         w = e / e.sum()
         out[h] = w @ vv[seen, kv]
         mag[h] = w @ np.abs(vv[seen, kv])
+        at = np.flatnonzero(seen) // BLOCK
+        top[h] = sum(w[at == j].max() * np.abs(vv[seen, kv][at == j]).max() for j in np.unique(at))
     if g is not None:
         sg = 1.0 / (1.0 + np.exp(-_f64(g)))
-        out, mag = out * sg, mag * sg
-    return out, lse, mag
+        out, mag, top = out * sg, mag * sg, top * sg.max(1)
+    return out, lse, mag, top
 
 
 def select(q, mean, *, first_block, n_select, n_first, n_last):

@@ -46,7 +46,7 @@ def test_norm_rope_is_the_layers_own():
     q = qkrope.forward(t["q"][0], t["gamma_q"], pos, **kw)
     k = qkrope.forward(t["k"][0], t["gamma_k"], pos, **kw)
     for i in range(9):
-        out, lse, _ = kv8.attend(q[i], t["g"][0, i], k[:i + 1], t["v"][0, :i + 1], code="e4m3", window=5, scale=0.25)
+        out, lse, *_ = kv8.attend(q[i], t["g"][0, i], k[:i + 1], t["v"][0, :i + 1], code="e4m3", window=5, scale=0.25)
         np.testing.assert_allclose(out, np.asarray(ref)[0, i], atol=1e-12)
         np.testing.assert_allclose(lse, np.asarray(ref_lse)[0, :, i], atol=1e-12)
 
@@ -80,13 +80,13 @@ def test_attend_reads_codes_and_tail():
     s = kv8.stored(k, "int8")
     assert np.array_equal(s[128:], k[128:]) and not np.array_equal(s[:128], k[:128])
     assert np.abs(s - k).max() <= np.abs(k).max() / 127 * 0.5001
-    out, lse, _ = kv8.attend(q, None, k, v, code="int8", window=10 ** 6)
+    out, lse, *_ = kv8.attend(q, None, k, v, code="int8", window=10 ** 6)
     x = torch.from_numpy(s[:, 0]) @ torch.from_numpy(q).T * 8 ** -0.5
     np.testing.assert_allclose(lse, torch.logsumexp(x, 0).numpy(), atol=1e-12)
     np.testing.assert_allclose(out, (torch.softmax(x, 0).T @ torch.from_numpy(kv8.stored(v, "int8")[:, 0])).numpy(),
                                atol=1e-12)
     # a list: block 1 and the own block
-    one, _, _ = kv8.attend(q, None, k, v, code="int8", window=10 ** 6, blocks=[[1, -1]])
+    one, *_ = kv8.attend(q, None, k, v, code="int8", window=10 ** 6, blocks=[[1, -1]])
     x = x[64:]
     np.testing.assert_allclose(one, (torch.softmax(x, 0).T @ torch.from_numpy(kv8.stored(v, "int8")[64:, 0])).numpy(),
                                atol=1e-12)
