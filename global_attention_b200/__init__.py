@@ -670,56 +670,77 @@ def zgcm_proj_out_bwd(a, w_o, dy, *, da=None, dw=None, stream=None):
 
 
 # ------------------------------------- q/k normalisation and rotation (zgcm_qkrope.h)
+#
+# These calls and those of zgcm_kv8.h run in decode steps of a few microseconds, so their checks
+# look at each tensor once and pass plain integers to ctypes.
+
+_NORM_TYPES = {}   # torch dtype -> zgcm_dtype
+
 
 def _type_code(t, name):
     import torch
-    for code, dtype in enumerate((torch.bfloat16, torch.float16, torch.float32)):
-        if t == dtype:
-            return code
-    raise TypeError(f"{name} must be bfloat16, float16 or float32")
+    if not _NORM_TYPES:
+        _NORM_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _NORM_TYPES.get(t)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32")
+    return code
 
 
-def _rows(t, name, dtype, shape):
-    """t: a [T, H, D] tensor of `dtype` whose rows of D are contiguous; its zgcm_rows.  Strides
-    of a dimension of one are not looked at (torch lets them be anything)."""
+def _is(t, name, dtype, shape, index):
+    """t: a contiguous tensor of `dtype` and exactly `shape` on CUDA device `index`; its address."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise TypeError(f"{name} must be a {dtype} tensor of rank 3 whose last dimension is contiguous")
-    if tuple(t.shape) != tuple(shape):
-        raise TypeError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
+                        f"{tuple(t.shape)}")
+    if t.get_device() != index:
+        raise _device_error(name, t, index)
+    return t.data_ptr()
 
 
-def _out_rows(t, name, dtype, shape):
-    """_rows of an output: no two of its elements in one place."""
-    r = _rows(t, name, dtype, shape)
-    (T, H, D) = shape
-    dims = sorted((s, n) for s, n in ((r.t_stride, T), (r.h_stride, H)) if n > 1)
-    reach = D
-    for s, n in dims:
-        if s < reach:
-            raise TypeError(f"{name} must not overlap itself")
-        reach = s * (n - 1) + reach
-    return r
+def _device_error(name, t, index):
+    if not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA tensor")
+    return TypeError(f"{name} must be on the device of the other tensors (cuda:{index})")
 
 
-class _on:
-    """Makes t's device the current one for the launches inside, where it is not already."""
+def _rows(t, name, dtype, shape, index, out=False):
+    """t: a [T, H, D] tensor of `dtype` on CUDA device `index` whose rows of D are contiguous; its zgcm_rows.  The
+    stride of a dimension of one is not looked at (torch lets it be anything).  out: no two elements in one place."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype or t.shape != shape:
+        raise TypeError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise _device_error(name, t, index)
+    T, H, D = shape
+    ts, hs, ds = t.stride()
+    if ds != 1 and D > 1:
+        raise TypeError(f"{name} must have contiguous rows")
+    if T <= 1:
+        ts = 0
+    if H <= 1:
+        hs = 0
+    if out and T > 0:
+        reach = D
+        for s, n in sorted(((ts, T), (hs, H))):
+            if n > 1:
+                if s < reach:
+                    raise TypeError(f"{name} must not overlap itself")
+                reach += s * (n - 1)
+    return _Rows(t.data_ptr(), ts, hs)
 
-    def __init__(self, t):
-        import torch
-        index = t.device.index
-        self.guard = None if index is None or index == torch.cuda.current_device() else torch.cuda.device(index)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _run(index, stream, fn, *args):
+    """fn(*args, stream) with device `index` current; stream: a torch stream or None (the device's current one)."""
+    import torch
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _run(index, stream, fn, *args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
 
 
 def _qk_check(q, k, gamma_q, gamma_k, pos):
@@ -727,13 +748,14 @@ def _qk_check(q, k, gamma_q, gamma_k, pos):
     for n, t in (("q", q), ("k", k)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise TypeError(f"{n} must be a tensor of rank 3")
-    (T, Hq, D), Hkv = q.shape, k.shape[1]
-    code = _type_code(q.dtype, "q")
-    rq, rk = _rows(q, "q", q.dtype, (T, Hq, D)), _rows(k, "k", q.dtype, (T, Hkv, D))
-    _need(gamma_q, "gamma_q", torch.float32, (D,))
-    _need(gamma_k, "gamma_k", torch.float32, (D,))
-    _need(pos, "pos", torch.int32, (T,))
-    return T, Hq, Hkv, D, code, rq, rk
+    T, Hq, D = q.shape
+    Hkv, dtype, index = k.shape[1], q.dtype, q.get_device()
+    code = _type_code(dtype, "q")
+    rq, rk = _rows(q, "q", dtype, (T, Hq, D), index), _rows(k, "k", dtype, (T, Hkv, D), index)
+    f32 = torch.float32
+    pg = _is(gamma_q, "gamma_q", f32, (D,), index), _is(gamma_k, "gamma_k", f32, (D,), index)
+    pp = _is(pos, "pos", torch.int32, (T,), index)
+    return T, Hq, Hkv, D, code, index, rq, rk, *pg, pp
 
 
 def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_base=10000.0, eps=1e-6, out_dtype=None,
@@ -742,25 +764,23 @@ def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_bas
     (bf16, fp16 or fp32, rows contiguous, any token and head strides that are multiples of 8), pos int32
     [T].  Returns (qr, kr) of out_dtype (default: q's), or writes the tensors given."""
     import torch
-    T, Hq, Hkv, D, xt, rq, rk = _qk_check(q, k, gamma_q, gamma_k, pos)
-    given = next((t for t in (qr, kr) if t is not None), None)
+    T, Hq, Hkv, D, xt, index, rq, rk, pgq, pgk, pp = _qk_check(q, k, gamma_q, gamma_k, pos)
     if out_dtype is None:
+        given = qr if qr is not None else kr
         out_dtype = q.dtype if given is None else given.dtype
     yt = _type_code(out_dtype, "out_dtype")
-    if given is not None:
-        for n, t, H in (("qr", qr, Hq), ("kr", kr, Hkv)):
-            if t is not None:
-                _out_rows(t, n, out_dtype, (T, H, D))
-    _one_device(("q", q), ("k", k), ("gamma_q", gamma_q), ("gamma_k", gamma_k), ("pos", pos), ("qr", qr), ("kr", kr))
+    rqr = None if qr is None else _rows(qr, "qr", out_dtype, (T, Hq, D), index, out=True)
+    rkr = None if kr is None else _rows(kr, "kr", out_dtype, (T, Hkv, D), index, out=True)
+    if index < 0:
+        raise TypeError("q must be a CUDA tensor")
     if qr is None:
         qr = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        rqr = _Rows(qr.data_ptr(), Hq * D, D)
     if kr is None:
         kr = torch.empty((T, Hkv, D), dtype=out_dtype, device=q.device)
-    with _on(q):
-        st = load().zgcm_qk_norm_rope_fwd(rq, rk, _ptr(gamma_q), _ptr(gamma_k), _ptr(pos), T, Hq, Hkv, D, xt, yt,
-                                          int(rope_dims), float(rope_base), float(eps),
-                                          _rows(qr, "qr", out_dtype, (T, Hq, D)),
-                                          _rows(kr, "kr", out_dtype, (T, Hkv, D)), _stream(stream))
+        rkr = _Rows(kr.data_ptr(), Hkv * D, D)
+    st = _run(index, stream, load().zgcm_qk_norm_rope_fwd, rq, rk, pgq, pgk, pp, T, Hq, Hkv, D, xt, yt, int(rope_dims),
+              float(rope_base), float(eps), rqr, rkr)
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_qk_norm_rope_fwd")
     return qr, kr
@@ -776,35 +796,33 @@ def zgcm_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, dqr, dkr, *, rope_dims=42
     """Gradients of zgcm_qk_norm_rope_fwd: dict dq, dk (q's dtype), dgamma_q, dgamma_k (fp32 [D], overwritten).
     `grads` may supply them, `workspace` a uint8 tensor of zgcm_qk_norm_rope_bwd_workspace_size(T) bytes."""
     import torch
-    T, Hq, Hkv, D, xt, rq, rk = _qk_check(q, k, gamma_q, gamma_k, pos)
+    T, Hq, Hkv, D, xt, index, rq, rk, pgq, pgk, pp = _qk_check(q, k, gamma_q, gamma_k, pos)
     if not isinstance(dqr, torch.Tensor):
         raise TypeError("dqr must be a torch tensor")
     yt = _type_code(dqr.dtype, "dqr")
-    rdq, rdk = _rows(dqr, "dqr", dqr.dtype, (T, Hq, D)), _rows(dkr, "dkr", dqr.dtype, (T, Hkv, D))
-    gl = []
-    if grads is not None:
-        _out_rows(grads["dq"], "dq", q.dtype, (T, Hq, D))
-        _out_rows(grads["dk"], "dk", q.dtype, (T, Hkv, D))
-        _need(grads["dgamma_q"], "dgamma_q", torch.float32, (D,))
-        _need(grads["dgamma_k"], "dgamma_k", torch.float32, (D,))
-        gl = [(n, grads[n]) for n in ("dq", "dk", "dgamma_q", "dgamma_k")]
+    rdqr = _rows(dqr, "dqr", dqr.dtype, (T, Hq, D), index)
+    rdkr = _rows(dkr, "dkr", dqr.dtype, (T, Hkv, D), index)
     if workspace is not None:
-        _check(workspace, "workspace", torch.uint8, 1, cuda=False)
-    _one_device(("q", q), ("k", k), ("gamma_q", gamma_q), ("gamma_k", gamma_k), ("pos", pos), ("dqr", dqr),
-                ("dkr", dkr), *gl, ("workspace", workspace))
+        _is(workspace, "workspace", torch.uint8, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else (), index)
+    if grads is not None:
+        rdq = _rows(grads["dq"], "dq", q.dtype, (T, Hq, D), index, out=True)
+        rdk = _rows(grads["dk"], "dk", q.dtype, (T, Hkv, D), index, out=True)
+        pdgq = _is(grads["dgamma_q"], "dgamma_q", torch.float32, (D,), index)
+        pdgk = _is(grads["dgamma_k"], "dgamma_k", torch.float32, (D,), index)
+    if index < 0:
+        raise TypeError("q must be a CUDA tensor")
     if grads is None:
-        grads = dict(dq=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
-                     dk=torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device),
-                     dgamma_q=torch.empty(D, dtype=torch.float32, device=q.device),
-                     dgamma_k=torch.empty(D, dtype=torch.float32, device=q.device))
+        dev = q.device
+        dq, dk = torch.empty((T, Hq, D), dtype=q.dtype, device=dev), torch.empty((T, Hkv, D), dtype=q.dtype, device=dev)
+        dgq, dgk = torch.empty(D, dtype=torch.float32, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
+        rdq, rdk = _Rows(dq.data_ptr(), Hq * D, D), _Rows(dk.data_ptr(), Hkv * D, D)
+        pdgq, pdgk = dgq.data_ptr(), dgk.data_ptr()
+        grads = {"dq": dq, "dk": dk, "dgamma_q": dgq, "dgamma_k": dgk}
+    lib = load()
     if workspace is None:
-        workspace = torch.empty(max(16, zgcm_qk_norm_rope_bwd_workspace_size(T)), dtype=torch.uint8, device=q.device)
-    with _on(q):
-        st = load().zgcm_qk_norm_rope_bwd(rq, rk, _ptr(gamma_q), _ptr(gamma_k), _ptr(pos), rdq, rdk, T, Hq, Hkv, D, xt,
-                                          yt, int(rope_dims), float(rope_base), float(eps),
-                                          _rows(grads["dq"], "dq", q.dtype, (T, Hq, D)),
-                                          _rows(grads["dk"], "dk", q.dtype, (T, Hkv, D)), _ptr(grads["dgamma_q"]),
-                                          _ptr(grads["dgamma_k"]), _ptr(workspace), workspace.numel(), _stream(stream))
+        workspace = torch.empty(max(16, lib.zgcm_qk_norm_rope_bwd_workspace_size(T)), dtype=torch.uint8, device=q.device)
+    st = _run(index, stream, lib.zgcm_qk_norm_rope_bwd, rq, rk, pgq, pgk, pp, rdqr, rdkr, T, Hq, Hkv, D, xt, yt,
+              int(rope_dims), float(rope_base), float(eps), rdq, rdk, pdgq, pdgk, workspace.data_ptr(), workspace.numel())
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_qk_norm_rope_bwd")
     return grads
@@ -852,7 +870,7 @@ class ZgcmKv8Cache:
         _one_device(*zip(self._NAMES, tensors))
         self._t = dict(zip(self._NAMES, tensors))
         self.n_seq, self.n_blocks, self.n_pages, self.Hkv, self.D = n_seq, n_blocks, P, Hkv, D
-        self.key_dtype, self.device = k_tail.dtype, k_codes.device
+        self.key_dtype, self.device, self._index = k_tail.dtype, k_codes.device, k_codes.get_device()
         self._c = _Kv8Struct(*(t.data_ptr() for t in tensors), n_seq, n_blocks, P, Hkv, D,
                              0 if k_codes.dtype == torch.float8_e4m3fn else 1, 0 if k_tail.dtype == torch.bfloat16 else 1)
         self._ref = ctypes.byref(self._c)
@@ -892,15 +910,32 @@ def zgcm_kv8_alloc(n_seq, n_blocks, Hkv, *, n_pages=None, D=128, code_dtype=None
                         torch.zeros(tails, dtype=torch.bfloat16, device=device), table)
 
 
-def _kv8_need(cache, *named):
-    """(name, tensor or None, dtype, shape): contiguous, of that shape, on the cache's device."""
+def _kv8_cache(cache):
     if not isinstance(cache, ZgcmKv8Cache):
         raise TypeError("cache must be a ZgcmKv8Cache")
-    for n, t, dtype, shape in named:
-        if t is not None:
-            _need(t, n, dtype, shape)
-            if t.device != cache.device:
-                raise TypeError(f"{n} must be on the cache's device ({cache.device}, a CUDA device)")
+    return cache._index
+
+
+def _kv8_query(cache, q):
+    """Query heads of q [n_seq, Hq, D]."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a tensor of rank 3")
+    return q.shape[1]
+
+
+def _kv8_tokens(cache, t, name, dtype, N, index):
+    """Address and strides of k or v [n_seq, N, Hkv, D] with contiguous rows."""
+    import torch
+    shape = (cache.n_seq, N, cache.Hkv, cache.D)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        raise TypeError(f"{name} must be a {dtype} tensor of shape {shape}")
+    if t.get_device() != index:
+        raise _device_error(name, t, index)
+    b, n, h, d = t.stride()
+    if d != 1 and cache.D > 1:
+        raise TypeError(f"{name} must have contiguous rows")
+    return t.data_ptr(), b if shape[0] > 1 else 0, n if N > 1 else 0, h if shape[2] > 1 else 0
 
 
 def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
@@ -908,21 +943,17 @@ def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
     contiguous, other strides multiples of 8; pos int32 [n_seq], the first token's position (negative: the sequence
     is idle); count int32 [n_seq], the tokens of each sequence (default N).  Updates the cache in place."""
     import torch
-    _kv8_need(cache)
-    for n, t, dtype in (("k", k, cache.key_dtype), ("v", v, torch.bfloat16)):
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-            raise TypeError(f"{n} must be a {dtype} tensor of rank 4 whose last dimension is contiguous")
-        if t.shape != (cache.n_seq, k.shape[1], cache.Hkv, cache.D):
-            raise TypeError(f"{n} must have shape {(cache.n_seq, k.shape[1], cache.Hkv, cache.D)}, not {tuple(t.shape)}")
-        if t.device != cache.device:
-            raise TypeError(f"{n} must be on the cache's device ({cache.device}, a CUDA device)")
-    _kv8_need(cache, ("pos", pos, torch.int32, (cache.n_seq,)), ("count", count, torch.int32, (cache.n_seq,)))
-    if not k.is_cuda:
+    index = _kv8_cache(cache)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise TypeError("k must be a tensor of rank 4")
+    N = k.shape[1]
+    pk = _kv8_tokens(cache, k, "k", cache.key_dtype, N, index)
+    pv = _kv8_tokens(cache, v, "v", torch.bfloat16, N, index)
+    pp = _is(pos, "pos", torch.int32, (cache.n_seq,), index)
+    pc = None if count is None else _is(count, "count", torch.int32, (cache.n_seq,), index)
+    if index < 0:
         raise TypeError("k must be a CUDA tensor")
-    ks, vs = ([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k, v))
-    with _on(k):
-        st = load().zgcm_kv8_append(cache._ref, _ptr(k), *ks, _ptr(v), *vs, _ptr(pos), _ptr(count), k.shape[1],
-                                    _stream(stream))
+    st = _run(index, stream, load().zgcm_kv8_append, cache._ref, *pk, *pv, pp, pc, N)
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_kv8_append")
     return cache
@@ -935,43 +966,45 @@ def zgcm_attn_decode_kv8_workspace_size(n_seq, Hq, Hkv) -> int:
 
 def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=None, out=None, lse=None, workspace=None,
                          stream=None):
-    """Decode attention of one token per sequence, appended before: q [n_seq,Hq,D] (cache.key_dtype, prepared),
+    """Decode attention of one token per sequence, the newest one appended: q [n_seq,Hq,D] (cache.key_dtype, prepared),
     g bf16 [n_seq,Hq,D] or None (no gate), pos int32 [n_seq].  blocks: int32 [n_seq,Hkv,n] from zgcm_kv8_select, the
     earlier blocks to read (default: all that the window reaches).  Returns (out bf16 [n_seq,Hq,D], lse fp32 [n_seq,Hq])."""
     import torch
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a tensor of rank 3")
-    _kv8_need(cache)
-    B, Hq, D = cache.n_seq, q.shape[1], cache.D
-    n_list = 0
+    index = _kv8_cache(cache)
+    Hq = _kv8_query(cache, q)
+    B, D = cache.n_seq, cache.D
+    shape = (B, Hq, D)
+    pq = _is(q, "q", cache.key_dtype, shape, index)
+    pg = None if g is None else _is(g, "g", torch.bfloat16, shape, index)
+    pp = _is(pos, "pos", torch.int32, (B,), index)
+    pb, n_list = None, 0
     if blocks is not None:
         if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3:
             raise TypeError("blocks must be a tensor of rank 3")
         n_list = blocks.shape[2]
-    _kv8_need(cache, ("q", q, cache.key_dtype, (B, Hq, D)), ("g", g, torch.bfloat16, (B, Hq, D)),
-              ("pos", pos, torch.int32, (B,)), ("blocks", blocks, torch.int32, (B, cache.Hkv, n_list)),
-              ("out", out, torch.bfloat16, (B, Hq, D)), ("lse", lse, torch.float32, (B, Hq)))
-    if not q.is_cuda:
+        pb = _is(blocks, "blocks", torch.int32, (B, cache.Hkv, n_list), index)
+        if n_list == 0:
+            pb = pp   # an empty list is not read: only that there is one counts
+    if out is not None:
+        _is(out, "out", torch.bfloat16, shape, index)
+    if lse is not None:
+        _is(lse, "lse", torch.float32, (B, Hq), index)
+    if workspace is not None:
+        _is(workspace, "workspace", torch.uint8, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else (), index)
+    if index < 0:
         raise TypeError("q must be a CUDA tensor")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    dev = cache.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    lib = load()
     if workspace is None:
-        workspace = torch.empty(max(16, zgcm_attn_decode_kv8_workspace_size(B, Hq, cache.Hkv)), dtype=torch.uint8,
-                                device=q.device)
-    else:
-        _check(workspace, "workspace", torch.uint8, 1, cuda=False)
-        if workspace.device != cache.device:
-            raise TypeError(f"workspace must be on the cache's device ({cache.device}, a CUDA device)")
-    if blocks is not None and n_list == 0:
-        blocks = pos   # an empty list: only whether there is one counts
-    with _on(q):
-        st = load().zgcm_attn_decode_kv8(cache._ref, _ptr(q), _ptr(g), _ptr(pos), _ptr(blocks), n_list, Hq, _window(window),
-                                         float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                         _stream(stream))
+        workspace = torch.empty(max(16, lib.zgcm_attn_decode_kv8_workspace_size(B, Hq, cache.Hkv)), dtype=torch.uint8,
+                                device=dev)
+    st = _run(index, stream, lib.zgcm_attn_decode_kv8, cache._ref, pq, pg, pp, pb, n_list, Hq, _window(window),
+              1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+              workspace.numel())
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_attn_decode_kv8")
     return out, lse
@@ -982,19 +1015,20 @@ def zgcm_kv8_select(cache, q, pos, n_select, *, n_first=1, n_last=1, window=128,
     zgcm_attn_decode_kv8(blocks=...).  q [n_seq,Hq,D] (cache.key_dtype, prepared); a block's score is the largest
     q . (mean of its keys) over the KV head's queries; the first n_first and last n_last candidates always count."""
     import torch
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a tensor of rank 3")
-    _kv8_need(cache)
-    B, n_select = cache.n_seq, int(n_select)
-    _kv8_need(cache, ("q", q, cache.key_dtype, (B, q.shape[1], cache.D)), ("pos", pos, torch.int32, (B,)),
-              ("out", out, torch.int32, (B, cache.Hkv, n_select)))
-    if not q.is_cuda:
+    index = _kv8_cache(cache)
+    Hq, n_select = _kv8_query(cache, q), int(n_select)
+    B = cache.n_seq
+    pq = _is(q, "q", cache.key_dtype, (B, Hq, cache.D), index)
+    pp = _is(pos, "pos", torch.int32, (B,), index)
+    shape = (B, cache.Hkv, max(0, n_select))
+    if out is not None:
+        _is(out, "out", torch.int32, shape, index)
+    if index < 0:
         raise TypeError("q must be a CUDA tensor")
     if out is None:
-        out = torch.empty((B, cache.Hkv, max(0, n_select)), dtype=torch.int32, device=q.device)
-    with _on(q):
-        st = load().zgcm_kv8_select(cache._ref, _ptr(q), _ptr(pos), q.shape[1], _window(window), n_select, int(n_first),
-                                    int(n_last), _ptr(out), _stream(stream))
+        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
+    st = _run(index, stream, load().zgcm_kv8_select, cache._ref, pq, pp, Hq, _window(window), n_select, int(n_first),
+              int(n_last), out.data_ptr())
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_kv8_select")
     return out

@@ -5,29 +5,38 @@
 //   u = R^T dy;  dgamma = sum u x r;  dx = r (gamma u - x r^2 mean(gamma u x))
 //
 // Bound by HBM: forward reads x and writes y, backward reads x and dy and writes dx, and no
-// value is used twice except by its own row.  A row of 128 belongs to 16 lanes, 8 elements
-// each (one 16-byte access of a 16-bit type), so its sums are 4 shuffles and it is read once.
-// The angles depend on the token alone: a CTA forms the cosines and sines of its few tokens
-// once (fp64 product and reduction: at position 262143 an fp32 product is off by 0.016 rad)
-// and each half-warp keeps its 8 pairs in registers over all the heads it takes of one token.
-// The partner of element d is d +- half, in another lane at an offset that depends on half: it
-// goes through shared memory, the rotated elements only.
+// value is used twice except by its own row.  What has to stay small beside it is the number of
+// instructions: at the rate of HBM an SM has 88 issue slots for a row forward.  So a row of
+// 128 belongs to 8 lanes, 16 elements each in two chunks (8 l .. and 64 + 8 l .., one 16-byte
+// access of a 16-bit type each): a warp works on 4 rows at once, their sums are 3 shuffles, and
+// the layer's rotated dims, 42 of 128, lie in the first chunks alone.  Two fp32 operations go in
+// one instruction.  gamma and the angles make two factors for an element and token,
+// y = (x A + x_partner B) r, kept in registers over the rows a warp takes of a token; the angles
+// are formed once a warp and token (fp64 product and reduction: at position 262143 an fp32 product
+// is off by 0.016 rad).  The partner of element d is d +- half, in another lane:
+//   half = 21 (the layer's) and 16-bit rows: two lanes and 5 elements up, or 3 elements past
+//     three lanes down: 5 words of the row as read from either side by shuffles, shifted by an element
+//     (kHalf21 instances);
+//   any other: the row's rotated elements go to shared memory as they were read, the first half
+//     of them a second time behind the last (the partner is d + half modulo 2 half), and a lane
+//     reads the partners of a chunk as one run of words.
 #include <math.h>
 
 #include <initializer_list>
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "sm100.cuh"
 #include "zgcm_qkrope.h"
 
 namespace zgcm {
 namespace {
 
 constexpr int QR_THREADS = 256;
-constexpr int QR_HW = QR_THREADS / 16;   // half-warps of a CTA
-constexpr int QR_MAX_TT = 4;             // tokens per CTA and step
-constexpr int QR_BWD_CTAS = 592;         // most CTAs of the backward (4 per SM), one dgamma partial each
+constexpr int QR_WARPS = QR_THREADS / 32;
+constexpr int QR_MAX_WPT = 16;           // most warps that share a token's rows
+constexpr int QR_BWD_CTAS = 296;         // most CTAs of the backward (2 per SM), one dgamma partial each
+constexpr int kHalf21 = 21;              // the layer's rope_dims / 2
 
 struct Rows {
     char* p;
@@ -40,239 +49,390 @@ struct QrParams {
     const float* gamma_k;
     const int* pos;
     float* part;                 // backward: [CTAs][2][128] partial dgamma
-    int T, Hq, Hkv, half, tt;    // tt: tokens per CTA step (a power of two, at most QR_MAX_TT)
+    int T, Hq, Hkv, half, wpt;   // wpt: warps of a token
     float eps;
     double turns[kMaxHalf];      // rope_base^(-2i/rope_dims) / 2 pi
 };
 
+// 8 elements of a row: kWords 32-bit words
 template <typename T> struct Vec8;
 template <> struct Vec8<bf16> {
+    static constexpr int kWords = 4;
     uint4 w;
+    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+    __device__ __forceinline__ void set(const uint32_t (&u)[4]) { w = make_uint4(u[0], u[1], u[2], u[3]); }
     __device__ __forceinline__ void load(const char* base, long long at) {
         w = *reinterpret_cast<const uint4*>(base + 2 * at);
     }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float f[8]) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 t = unpack_bf16(u[i]);
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
-        }
+    __device__ __forceinline__ void get(float2 f[4]) const {
+        f[0] = unpack_bf16(w.x);
+        f[1] = unpack_bf16(w.y);
+        f[2] = unpack_bf16(w.z);
+        f[3] = unpack_bf16(w.w);
     }
-    static __device__ __forceinline__ void store(char* base, long long at, const float f[8]) {
-        *reinterpret_cast<uint4*>(base + 2 * at) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                              pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    static __device__ __forceinline__ void store(char* base, long long at, const float2 f[4]) {
+        *reinterpret_cast<uint4*>(base + 2 * at) = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y),
+                                                              pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
     }
 };
 template <> struct Vec8<__half> {
+    static constexpr int kWords = 4;
     uint4 w;
+    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+    __device__ __forceinline__ void set(const uint32_t (&u)[4]) { w = make_uint4(u[0], u[1], u[2], u[3]); }
     __device__ __forceinline__ void load(const char* base, long long at) {
         w = *reinterpret_cast<const uint4*>(base + 2 * at);
     }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float f[8]) const {
+    __device__ __forceinline__ void get(float2 f[4]) const {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
-        }
+        for (int i = 0; i < 4; ++i) f[i] = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
     }
-    static __device__ __forceinline__ void store(char* base, long long at, const float f[8]) {
+    static __device__ __forceinline__ void store(char* base, long long at, const float2 f[4]) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            const __half2 h = __float22half2_rn(f[i]);
             u[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         *reinterpret_cast<uint4*>(base + 2 * at) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
 template <> struct Vec8<float> {
+    static constexpr int kWords = 8;
     float4 a, b;
+    __device__ __forceinline__ uint32_t word(int i) const {
+        const float4& q = i < 4 ? a : b;
+        const int j = i & 3;
+        return __float_as_uint(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
+    }
+    __device__ __forceinline__ void set(const uint32_t (&u)[8]) {
+        a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3]));
+        b = make_float4(__uint_as_float(u[4]), __uint_as_float(u[5]), __uint_as_float(u[6]), __uint_as_float(u[7]));
+    }
     __device__ __forceinline__ void load(const char* base, long long at) {
         a = *reinterpret_cast<const float4*>(base + 4 * at);
         b = *reinterpret_cast<const float4*>(base + 4 * at + 16);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float f[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void get(float2 f[4]) const {
+        f[0] = make_float2(a.x, a.y);
+        f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y);
+        f[3] = make_float2(b.z, b.w);
     }
-    static __device__ __forceinline__ void store(char* base, long long at, const float f[8]) {
-        *reinterpret_cast<float4*>(base + 4 * at) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(base + 4 * at + 16) = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(char* base, long long at, const float2 f[4]) {
+        *reinterpret_cast<float4*>(base + 4 * at) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        *reinterpret_cast<float4*>(base + 4 * at + 16) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
 };
 
-__device__ __forceinline__ float sum16(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 8);
+__device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 4);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x;
 }
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-struct QrSmem {
-    float2 cs[QR_MAX_TT][kMaxHalf];
-    __align__(16) float swap[QR_HW][2][kD + 4];  // [half-warp][row parity]: rotated elements on their way to partners
+// Words of a row in the exchange buffer: 128 + 64 elements and the window of the last lane past them
+template <typename T> constexpr int kPitch = (kD + kD / 2 + 8) * Vec8<T>::kWords / 8 + 2;
+
+template <typename T, bool H21> struct QrSmem {
+    __align__(16) float gamma[2][kD];
+    __align__(16) float2 cs[QR_WARPS][kMaxHalf];               // cosine and sine of the warp's token
+    uint32_t ring[H21 ? 1 : QR_WARPS][4][H21 ? 1 : kPitch<T>]; // [warp][row]: its rotated elements
 };
 
-// cosines and sines of the CTA's tokens t0 .. t0 + tt - 1
-__device__ __forceinline__ void fill_angles(const QrParams& p, QrSmem& sm, int t0) {
-    for (int i = threadIdx.x; i < p.tt * p.half; i += QR_THREADS) {
-        const int t = i / p.half, j = i % p.half;
-        if (t0 + t < p.T) {
-            const double a = (double)p.pos[t0 + t] * p.turns[j];
-            float s, c;
-            sincospif(2.0f * (float)(a - rint(a)), &s, &c);
-            sm.cs[t][j] = make_float2(c, s);
-        }
+template <typename T, bool H21> __device__ __forceinline__ void fill_smem(const QrParams& p, QrSmem<T, H21>& sm) {
+    sm.gamma[threadIdx.x >> 7][threadIdx.x & 127] = (threadIdx.x < kD ? p.gamma_q : p.gamma_k)[threadIdx.x & 127];
+    if (!H21) {
+        // a lane at the end of the rotated elements reads words that no row writes, against a factor of zero: not NaN
+        uint32_t* w = &sm.ring[0][0][0];
+        for (int i = threadIdx.x; i < (int)(sizeof(sm.ring) / 4); i += QR_THREADS) w[i] = 0u;
     }
+    __syncthreads();
 }
 
-// this lane's 8 (cos, signed sin): y_d' = y_d c + y_partner s, s negative in the first half
-__device__ __forceinline__ void lane_angles(const QrSmem& sm, int t, int l, int half, float c[8], float s[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int d = 8 * l + e;
-        c[e] = 1.f;
-        s[e] = 0.f;
-        if (d < 2 * half) {
-            const float2 v = sm.cs[t][d < half ? d : d - half];
-            c[e] = v.x;
-            s[e] = d < half ? -v.y : v.y;
-        }
-    }
-}
-
-// z[e] = y[e] c[e] + sign * y[partner of e] s[e].  `buf`: this half-warp's row buffer, not in use by the
-// row before (callers alternate two); every lane of the warp calls it.
-__device__ __forceinline__ void rotate(float y[8], const float c[8], const float s[8], float sign, float* buf, int l,
-                                       int half) {
-    const bool rot = 8 * l < 2 * half;
-    if (rot) {
-        *reinterpret_cast<float4*>(buf + 8 * l) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4*>(buf + 8 * l + 4) = make_float4(y[4], y[5], y[6], y[7]);
+__device__ __forceinline__ void angles(const QrParams& p, float2* cs, int t) {
+    const double pos = (double)p.pos[t];
+    __syncwarp();   // the token before has been read
+    for (int j = threadIdx.x & 31; j < p.half; j += 32) {
+        const double a = pos * p.turns[j];
+        float sn, co;
+        sincospif(2.0f * (float)(a - rint(a)), &sn, &co);
+        cs[j] = make_float2(co, sn);
     }
     __syncwarp();
-    if (rot) {
+}
+
+// Factors of the 8 elements from d0: y_d' = y_d a + y_partner b.  gamma (may be null) is that of y; b has the
+// partner's.
+template <int SIGN>
+__device__ __forceinline__ void factors(const float2* cs, const float* gamma, int d0, int half, float2 a[4], float2 b[4]) {
+    float x[8], y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int d = 8 * l + e;
-            if (d < 2 * half) y[e] = fmaf(buf[d < half ? d + half : d - half], sign * s[e], y[e] * c[e]);
+    for (int e = 0; e < 8; ++e) {
+        const int d = d0 + e;
+        x[e] = gamma ? gamma[d] : 1.f;
+        y[e] = 0.f;
+        if (d < 2 * half) {
+            const float2 w = cs[d < half ? d : d - half];
+            x[e] *= w.x;
+            y[e] = (d < half ? -SIGN : SIGN) * w.y * (gamma ? gamma[d < half ? d + half : d - half] : 1.f);
         }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = make_float2(x[2 * e], x[2 * e + 1]);
+        b[e] = make_float2(y[2 * e], y[2 * e + 1]);
     }
 }
 
-template <typename X, typename Y>
-__global__ void __launch_bounds__(QR_THREADS) qk_norm_rope_fwd_kernel(const __grid_constant__ QrParams p) {
-    __shared__ QrSmem sm;
-    const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
-    const int hpt = QR_HW / p.tt;                 // half-warps of a token
-    const int tl = hw / hpt, part = hw % hpt;
-    const int t = blockIdx.x * p.tt + tl;
-    fill_angles(p, sm, blockIdx.x * p.tt);
-    __syncthreads();
-    float c[8], s[8];
-    lane_angles(sm, tl, l, p.half, c, s);
-    for (int side = 0; side < 2; ++side) {
-        const Rows& x = side ? p.k : p.q;
-        const Rows& y = side ? p.yk : p.yq;
-        const int H = side ? p.Hkv : p.Hq;
-        float g[8];
+// Partners of the 8 elements of a first chunk, half = 21.  (A lane past the rotated ones gets elements of its own row,
+// against a factor of zero.)
+template <typename T> struct Partner21 {
+    int up2, up3, dn3, dn2;    // lanes of the warp
+    uint32_t first[4];         // the elements of each word that are below 21
+    __device__ __forceinline__ Partner21() {
+        const int lane = threadIdx.x & 31, l = lane & 7, row = lane & 24;
+        up2 = row | ((l + 2) & 7);
+        up3 = row | ((l + 3) & 7);
+        dn3 = row | ((l - 3) & 7);
+        dn2 = row | ((l - 2) & 7);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = (side ? p.gamma_k : p.gamma_q)[8 * l + e];
-        for (int h0 = 0, it = 0; h0 < H; h0 += hpt, ++it) {
-            const int h = h0 + part;
-            const bool on = t < p.T && h < H;
-            Vec8<X> v;
-            v.zero();
-            if (on) v.load(x.p, t * x.ts + h * x.hs + 8 * l);
-            float f[8], ss = 0.f;
-            v.get(f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-            const float r = rsqrtf(sum16(ss) * (1.0f / kD) + p.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * r * g[e];
-            rotate(f, c, s, 1.f, sm.swap[hw][it & 1], l, p.half);
-            if (on) Vec8<Y>::store(y.p, t * y.ts + h * y.hs + 8 * l, f);
+        for (int i = 0; i < 4; ++i) {
+            const int d = 8 * l + 2 * i;
+            first[i] = (d < kHalf21 ? 0xffffu : 0u) | (d + 1 < kHalf21 ? 0xffff0000u : 0u);
         }
-        __syncwarp();
     }
-}
+    __device__ __forceinline__ void get(const Vec8<T>& v, float2 y[4]) const {
+        const uint32_t m = 0xffffffffu;
+        // elements 5 .. 12 from two lanes up
+        const uint32_t p[5] = {__shfl_sync(m, v.word(2), up2), __shfl_sync(m, v.word(3), up2), __shfl_sync(m, v.word(0), up3),
+                               __shfl_sync(m, v.word(1), up3), __shfl_sync(m, v.word(2), up3)};
+        // elements 3 .. 10 from three lanes down
+        const uint32_t q[5] = {__shfl_sync(m, v.word(1), dn3), __shfl_sync(m, v.word(2), dn3), __shfl_sync(m, v.word(3), dn3),
+                               __shfl_sync(m, v.word(0), dn2), __shfl_sync(m, v.word(1), dn2)};
+        uint32_t u[Vec8<T>::kWords];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = (__funnelshift_r(p[i], p[i + 1], 16) & first[i]) | (__funnelshift_r(q[i], q[i + 1], 16) & ~first[i]);
+        Vec8<T> o;
+        o.set(u);
+        o.get(y);
+    }
+};
 
-template <typename X, typename Y>
-__global__ void __launch_bounds__(QR_THREADS) qk_norm_rope_bwd_kernel(const __grid_constant__ QrParams p) {
-    __shared__ QrSmem sm;
-    __shared__ float red[QR_HW][kD];
-    const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
-    const int hpt = QR_HW / p.tt;
-    const int tl = hw / hpt, part = hw % hpt;
-    float dg[2][8] = {};
-    for (int t0 = blockIdx.x * p.tt; t0 < p.T; t0 += gridDim.x * p.tt) {
-        const int t = t0 + tl;
-        __syncthreads();   // the step before has read its angles
-        fill_angles(p, sm, t0);
-        __syncthreads();
-        float c[8], s[8];
-        lane_angles(sm, tl, l, p.half, c, s);
+// Partners of both chunks of a row by the exchange buffer; every lane of the warp calls it.
+template <typename T>
+__device__ __forceinline__ void partners(const Vec8<T> (&v)[2], float2 (&y)[2][4], uint32_t* ring, int l, int half) {
+    constexpr int W = Vec8<T>::kWords, per = 8 / W;      // elements of a word
+    const int n = 2 * half / per, behind = (half + per - 1) / per;   // words of a row; of its first half
+    __syncwarp();   // the row before has been read
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const Rows& x = side ? p.k : p.q;
-            const Rows& dy = side ? p.yk : p.yq;
-            const Rows& dx = side ? p.dk : p.dq;
-            const int H = side ? p.Hkv : p.Hq;
-            float g[8];
+    for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = (side ? p.gamma_k : p.gamma_q)[8 * l + e];
-            for (int h0 = 0, it = 0; h0 < H; h0 += hpt, ++it) {
-                const int h = h0 + part;
-                const bool on = t < p.T && h < H;
-                Vec8<X> v;
-                Vec8<Y> w;
-                v.zero();
-                w.zero();
-                if (on) {
-                    v.load(x.p, t * x.ts + h * x.hs + 8 * l);
-                    w.load(dy.p, t * dy.ts + h * dy.hs + 8 * l);
-                }
-                float f[8], u[8], ss = 0.f, sx = 0.f;
-                v.get(f);
-                w.get(u);
-                rotate(u, c, s, -1.f, sm.swap[hw][it & 1], l, p.half);
+        for (int i = 0; i < W; ++i) {
+            const int w = 8 * W * ch + W * l + i;
+            if (w < n) ring[w] = v[ch].word(i);
+            if (w < behind) ring[n + w] = v[ch].word(i);
+        }
+    __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(f[e], f[e], ss);
-                    sx = fmaf(f[e], u[e] * g[e], sx);
-                }
-                ss = sum16(ss);
-                sx = sum16(sx);
-                const float r = rsqrtf(ss * (1.0f / kD) + p.eps);
-                const float m = r * r * sx * (1.0f / kD);     // r mean(gamma u xhat)
+    for (int ch = 0; ch < 2; ++ch) {
+        const int w0 = 8 * W * ch + W * l;
+        uint32_t u[W];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (on) dg[side][e] = fmaf(u[e], f[e] * r, dg[side][e]);
-                    u[e] = r * fmaf(-f[e], m, u[e] * g[e]);
-                }
-                if (on) Vec8<X>::store(dx.p, t * dx.ts + h * dx.hs + 8 * l, u);
+        for (int i = 0; i < W; ++i) u[i] = 0u;
+        if (w0 < n) {
+            const uint32_t* at = ring + w0 + half / per;
+#pragma unroll
+            for (int i = 0; i < W; ++i) u[i] = at[i];
+            if (per == 2) {
+                const int shift = (half & 1) * 16;
+                const uint32_t last = at[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) u[i] = __funnelshift_r(u[i], i + 1 < W ? u[i + 1] : last, shift);
             }
-            __syncwarp();
+        }
+        Vec8<T> o;
+        o.set(u);
+        o.get(y[ch]);
+    }
+}
+
+// Row h of a token's q and k counted through: nothing past the last.
+template <typename X>
+__device__ __forceinline__ void load_row(const Rows& q, const Rows& k, int Hq, int H, Vec8<X> (&v)[2], int t, int h, int l) {
+    v[0].zero();
+    v[1].zero();
+    if (h < H) {
+        const Rows& x = h < Hq ? q : k;
+        const long long at = t * x.ts + (h < Hq ? h : h - Hq) * x.hs + 8 * l;
+        v[0].load(x.p, at);
+        v[1].load(x.p, at + 64);
+    }
+}
+
+// A warp takes a token, or one of wpt shares of its rows, q and k counted through, 4 rows at a time and the next 4
+// already on their way.
+template <typename X, typename Y, bool H21>
+__global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const __grid_constant__ QrParams p) {
+    __shared__ QrSmem<X, H21> sm;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
+    fill_smem(p, sm);
+    const long long unit = (long long)blockIdx.x * QR_WARPS + warp;
+    const int t = (int)(unit / p.wpt), share = (int)(unit % p.wpt);
+    if (t >= p.T) return;
+    const int H = p.Hq + p.Hkv, step = 4 * p.wpt;
+    Vec8<X> next[2];
+    load_row(p.q, p.k, p.Hq, H, next, t, 4 * share + row, l);
+    angles(p, sm.cs[warp], t);
+    const Partner21<X> p21;
+    float2 a[2][4], b[2][4];
+    int side = -1;   // whose factors a, b are
+    for (int base = 4 * share; base < H; base += step) {
+        const int h = base + row;
+        Vec8<X> v[2] = {next[0], next[1]};
+        load_row(p.q, p.k, p.Hq, H, next, t, h + step, l);
+        if (side != (h >= p.Hq)) {
+            side = h >= p.Hq;
+            const float* g = sm.gamma[side];
+            factors<1>(sm.cs[warp], g, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
+            factors<1>(sm.cs[warp], g, 64 + 8 * l, H21 ? kHalf21 : p.half, a[1], b[1]);
+        }
+        float2 f[2][4], y[2][4];
+        v[0].get(f[0]);
+        v[1].get(f[1]);
+        if (H21)
+            p21.get(v[0], y[0]);
+        else
+            partners(v, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
+        float2 ss = sm100::fmul2(f[0][0], f[0][0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) ss = sm100::ffma2(f[e >> 2][e & 3], f[e >> 2][e & 3], ss);
+        const float2 r = pair(rsqrtf(sum8(ss.x + ss.y) * (1.0f / kD) + p.eps));
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 z = sm100::fmul2(f[ch][e], a[ch][e]);
+                if (!H21 || ch == 0) z = sm100::ffma2(y[ch][e], b[ch][e], z);
+                f[ch][e] = sm100::fmul2(z, r);
+            }
+        if (h < H) {
+            const Rows& o = h < p.Hq ? p.yq : p.yk;
+            const long long at = t * o.ts + (h < p.Hq ? h : h - p.Hq) * o.hs + 8 * l;
+            Vec8<Y>::store(o.p, at, f[0]);
+            Vec8<Y>::store(o.p, at + 64, f[1]);
         }
     }
+}
+
+// As the forward.  dgamma: this lane's 16 sums over its q rows in registers, those over its k rows, a quarter as
+// many in the layer, in shared memory; the CTA's partials at the end.
+template <typename X, typename Y, bool H21>
+__global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QrParams p) {
+    __shared__ QrSmem<Y, H21> sm;
+    __shared__ float4 dgk[QR_WARPS][4][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
+    fill_smem(p, sm);
+    float2 dg[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dgk[warp][i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const Partner21<Y> p21;
+    const int H = p.Hq + p.Hkv, step = 4 * p.wpt;
+    const long long units = (long long)p.T * p.wpt;
+    for (long long unit = (long long)blockIdx.x * QR_WARPS + warp; unit < units; unit += (long long)gridDim.x * QR_WARPS) {
+        const int t = (int)(unit / p.wpt), share = (int)(unit % p.wpt);
+        Vec8<X> nv[2];
+        Vec8<Y> nw[2];
+        load_row(p.q, p.k, p.Hq, H, nv, t, 4 * share + row, l);
+        load_row(p.yq, p.yk, p.Hq, H, nw, t, 4 * share + row, l);
+        float2 a[2][4], b[2][4];
+        angles(p, sm.cs[warp], t);
+        factors<-1>(sm.cs[warp], nullptr, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
+        if (!H21) factors<-1>(sm.cs[warp], nullptr, 64 + 8 * l, p.half, a[1], b[1]);
+        for (int base = 4 * share; base < H; base += step) {
+            const int h = base + row;
+            const Vec8<X> v[2] = {nv[0], nv[1]};
+            const Vec8<Y> w[2] = {nw[0], nw[1]};
+            load_row(p.q, p.k, p.Hq, H, nv, t, h + step, l);
+            load_row(p.yq, p.yk, p.Hq, H, nw, t, h + step, l);
+            float2 f[2][4], u[2][4], y[2][4], ug[2][4];
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                v[ch].get(f[ch]);
+                w[ch].get(u[ch]);
+            }
+            if (H21)
+                p21.get(w[0], y[0]);
+            else
+                partners(w, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
+            const float* g = sm.gamma[h < p.Hq ? 0 : 1] + 8 * l;
+            float2 ss = pair(0.f), sx = pair(0.f);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!H21 || ch == 0) u[ch][e] = sm100::ffma2(y[ch][e], b[ch][e], sm100::fmul2(u[ch][e], a[ch][e]));
+                    ug[ch][e] = sm100::fmul2(u[ch][e], *reinterpret_cast<const float2*>(g + 64 * ch + 2 * e));
+                    ss = sm100::ffma2(f[ch][e], f[ch][e], ss);
+                    sx = sm100::ffma2(f[ch][e], ug[ch][e], sx);
+                }
+            const float sq = sum8(ss.x + ss.y), sd = sum8(sx.x + sx.y);
+            const float r = rsqrtf(sq * (1.0f / kD) + p.eps);
+            const float2 m = pair(-r * r * sd * (1.0f / kD)), rr = pair(r);     // m = -r mean(gamma u xhat)
+            if (h < H) {
+                const bool isq = h < p.Hq;
+                const Rows& o = isq ? p.dq : p.dk;
+                const long long at = t * o.ts + (isq ? h : h - p.Hq) * o.hs + 8 * l;
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        ug[ch][e] = sm100::fmul2(rr, sm100::ffma2(f[ch][e], m, ug[ch][e]));
+                        f[ch][e] = sm100::fmul2(u[ch][e], sm100::fmul2(f[ch][e], rr));       // dgamma's term
+                    }
+                    Vec8<X>::store(o.p, at + 64 * ch, ug[ch]);
+                }
+                if (isq) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dg[e >> 2][e & 3] = sm100::fadd2(dg[e >> 2][e & 3], f[e >> 2][e & 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float4& s = dgk[warp][i][lane];
+                        const float2 x = f[i >> 1][2 * (i & 1)], z = f[i >> 1][2 * (i & 1) + 1];
+                        s = make_float4(s.x + x.x, s.y + x.y, s.z + z.x, s.w + z.y);
+                    }
+                }
+            }
+        }
+    }
+    // the CTA's sums, in a fixed order; the angles' place is free then
+    float(*red)[kD] = reinterpret_cast<float(*)[kD]>(sm.cs);
+    static_assert(sizeof(sm.cs) == QR_WARPS * kD * sizeof(float), "one row of 128 sums a warp");
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[hw][8 * l + e] = dg[side][e];
+        for (int i = 0; i < 16; ++i) {
+            const float2 v = dg[i >> 3][(i >> 1) & 3];
+            float x = (i & 1) ? v.y : v.x;
+            if (side) x = reinterpret_cast<const float*>(&dgk[warp][i >> 2][lane])[i & 3];
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (lane < 8) red[warp][64 * (i >> 3) + 8 * l + (i & 7)] = x;
+        }
         __syncthreads();
         if (threadIdx.x < kD) {
-            float a = 0.f;
-            for (int i = 0; i < QR_HW; ++i) a += red[i][threadIdx.x];
-            p.part[((size_t)blockIdx.x * 2 + side) * kD + threadIdx.x] = a;
+            float x = 0.f;
+            for (int i = 0; i < QR_WARPS; ++i) x += red[i][threadIdx.x];
+            p.part[((size_t)blockIdx.x * 2 + side) * kD + threadIdx.x] = x;
         }
     }
 }
@@ -292,23 +452,34 @@ __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float* part, int n
     }
 }
 
-// Tokens per CTA step: one while that leaves CTAs for every SM, else 4 (the angles of 4
-// tokens fill half the CTA's threads and the 40 rows of each go to 4 half-warps).
-int tokens_per_step(int T) { return T <= 592 ? 1 : QR_MAX_TT; }
+// Warps of a token: the most that still leaves each its own warp on an SM (16 a SM, 148 SMs), so that a decode
+// step's few tokens spread over the GPU; one for long batches (the angles are formed once a warp).
+int warps_per_token(int T) {
+    int n = QR_MAX_WPT;
+    while (n > 1 && (long long)T * n > 148 * 16) n /= 2;
+    return n;
+}
+
+int fwd_ctas(int T) { return (int)(((long long)T * warps_per_token(T) + QR_WARPS - 1) / QR_WARPS); }
 
 int bwd_ctas(int T) {
-    const int tt = tokens_per_step(T);
-    const int n = (T + tt - 1) / tt;
+    const int n = fwd_ctas(T);
     return n < QR_BWD_CTAS ? n : QR_BWD_CTAS;
 }
 
 template <typename X, typename Y>
 cudaError_t launch(const QrParams& p, bool bwd, cudaStream_t stream) {
-    if (bwd) {
-        qk_norm_rope_bwd_kernel<X, Y><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
-    } else {
-        qk_norm_rope_fwd_kernel<X, Y><<<(p.T + p.tt - 1) / p.tt, QR_THREADS, 0, stream>>>(p);
-    }
+    // the type whose rows are exchanged: x forward, dy backward
+    constexpr bool fwd16 = sizeof(X) == 2, bwd16 = sizeof(Y) == 2;
+    const bool h21 = p.half == kHalf21;
+    if (!bwd && fwd16 && h21)
+        qk_norm_rope_fwd_kernel<X, Y, fwd16><<<fwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
+    else if (!bwd)
+        qk_norm_rope_fwd_kernel<X, Y, false><<<fwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
+    else if (bwd16 && h21)
+        qk_norm_rope_bwd_kernel<X, Y, bwd16><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
+    else
+        qk_norm_rope_bwd_kernel<X, Y, false><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -360,7 +531,7 @@ void fill(QrParams& p, zgcm_rows q, zgcm_rows k, const float* gamma_q, const flo
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.half = rope_dims / 2;
-    p.tt = tokens_per_step(T);
+    p.wpt = warps_per_token(T);
     p.eps = eps;
     for (int i = 0; i < kMaxHalf; ++i)
         p.turns[i] = i < p.half ? pow(rope_base, -2.0 * i / rope_dims) * 0.15915494309189535 : 0.0;
