@@ -11,7 +11,10 @@
 //   O = P V:   A = p in two 16-bit halves, rows 0-7 the rounded p, rows 8-15 what the rounding
 //              left (so the idle rows carry p to 22 bits), B = 16 keys x 8 dims.
 // Codes become fp16 exactly and their scales multiply the fp32 sums, once per block: the scores by
-// ks, the block's O by vs where it joins the running O.  q as bf16 is first multiplied by a
+// ks, the block's O by vs where it joins the running O.  E4M3 pairs are converted by one instruction;
+// an INT8 code x as the byte x + 128 under the exponent of 1024, less 1152 (taking the 128 off the
+// accumulators instead saves 2 of 5 instructions but not the bits that 128 sum p costs them: out was off by 2^-16
+// of a block's largest value).  q as bf16 is first multiplied by a
 // power of two that brings the row's largest element to 2^14 (exact but for elements 2^-28 of it).
 //
 // Work: the blocks of every (sequence, KV head, 8 heads) — an item — and its tail are laid end to end
@@ -25,65 +28,22 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include "kv8.cuh"
-#include "sm100.cuh"
-#include "tc_rows.cuh"
+#include "kv8_attn.cuh"
 
 namespace zgcm {
 int* library_error_word();  // zgcm_attn.cu: the site of an expired bounded wait
+bool kv8_direct_plan(DecodeKv8Params& p, int units);   // kv8_direct.cu
+cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream);
 
 namespace {
-using namespace sm100;
 
 constexpr int DK_CTAS = 296;               // 148 SMs x 2
 constexpr int DK_WARPS = 4;                // warps that compute; one more loads
 constexpr int DK_THREADS = (DK_WARPS + 1) * 32;
 constexpr int DK_STAGES = 6;
 constexpr int DK_POS = 64;                 // positions of the run's sequences kept in shared memory
-constexpr int DK_HEADS = 8;                // heads of an item
 constexpr int DK_REC = kD + 4;             // floats of a record's head: m, l, 2 pad, O
-constexpr float kInvP = 1.f / 16384.f;       // p is held times 2^14: as fp16 above its subnormals
 constexpr int DK_WAIT_LOAD = 0x810, DK_WAIT_RING = 0x811;
-
-struct DecodeKv8Params {
-    CUtensorMap tm_k, tm_v;                // [n_pages * Hkv * 64, 128] bytes, box 64 rows
-    Kv8 c;
-    const void* q;
-    const bf16* g;
-    const int* pos;
-    const int* blocks;
-    int n_list, Hq, G, HT, W;              // HT: items of a KV head (8 heads each)
-    int rows;                              // heads a record has room for: min(G, 8)
-    float scale_log2;
-    bf16* out;
-    float* lse;
-    float* part;                           // records [item + CTA][rows][DK_REC]
-    int* err;
-};
-
-// What a position asks for: its own block, the first block and key its window reaches, and the
-// units of one item: blocks to read (some of a list may turn out to be passed over) + 1 for the tail.
-struct Span {
-    int own, lo, jlo, units;
-    bool idle, bad;
-};
-
-__device__ __forceinline__ Span span_of(const DecodeKv8Params& p, int pos) {
-    Span s;
-    s.idle = pos < 0;
-    s.own = s.idle ? 0 : pos / kBlk;
-    s.lo = s.idle ? 0 : max(0, pos - p.W + 1);
-    s.jlo = s.lo / kBlk;
-    s.bad = s.own - s.jlo >= p.c.NB;
-    s.units = s.idle || s.bad ? 1 : (p.blocks ? p.n_list : s.own - s.jlo) + 1;
-    return s;
-}
-
-struct Meta {
-    float ks, vs;
-    int j;        // block, or -1: passed over
-    int pad;
-};
 
 struct DecodeSmem {
     alignas(1024) unsigned char k[DK_STAGES][kBlkBytes];
@@ -99,86 +59,6 @@ struct DecodeSmem {
 };
 static_assert(2 * (sizeof(DecodeSmem) + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
 
-// ------------------------------------------------------------------ tensor-core and code helpers
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-template <bool BF>
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    if (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// four codes -> two pairs of fp16 (bytes 0,1 and 2,3), exact
-template <int CODE> __device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if (CODE == ZGCM_E4M3) {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    } else {
-        // a byte u = x + 128 under the exponent byte 0x64 is the fp16 1024 + u
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-        lo = *reinterpret_cast<const uint32_t*>(&x);
-        hi = *reinterpret_cast<const uint32_t*>(&y);
-    }
-}
-
-template <typename TK> struct KeyType;
-template <> struct KeyType<__half> {
-    static constexpr bool kBf = false;
-    static __device__ __forceinline__ float2 unpack(uint32_t u) {
-        return __half22float2(*reinterpret_cast<const __half2*>(&u));
-    }
-};
-template <> struct KeyType<bf16> {
-    static constexpr bool kBf = true;
-    static __device__ __forceinline__ float2 unpack(uint32_t u) { return unpack_bf16(u); }
-};
-
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// a pair of values as a 16-bit pair and the pair of what the rounding left
-template <bool BF> __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    if (BF) {
-        hi = pack_bf16(a, b);
-        const float2 r = unpack_bf16(hi);
-        lo = pack_bf16(a - r.x, b - r.y);
-    } else {
-        hi = pack_half(a, b);
-        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        lo = pack_half(a - r.x, b - r.y);
-    }
-}
-
-__device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
 __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the walk over the units
@@ -242,30 +122,14 @@ __device__ __forceinline__ void load_run(const DecodeKv8Params& p, DecodeSmem& s
     for (long long x = lo; x < hi && ok; x += 32) {
         Walk w = at;
         run.step(w, lane);
-        int page = -1, j = -1, kvh = 0;
+        Tile tile{-1, -1, 0.f, 0.f};
         bool is8 = false;
-        float ks = 0.f, vs = 0.f;
+        int kvh = 0;
         if (x + lane < hi) {
             const Span s = span_of(p, run.pos(w.b));
             is8 = w.off < s.units - 1;
-            if (is8) {
-                kvh = w.rest / p.HT;
-                if (p.blocks) {
-                    const int* list = p.blocks + ((size_t)w.b * p.c.Hkv + kvh) * p.n_list + w.off;
-                    j = *list;
-                    if (j < s.jlo || j >= s.own || (w.off > 0 && j <= list[-1])) j = -1;
-                } else {
-                    j = s.jlo + w.off;
-                }
-                if (j >= 0) {
-                    page = kv8_page(p.c, w.b, j);
-                    ks = vs = NAN;          // a bad page reads as NaN
-                    if (page >= 0) {
-                        ks = p.c.ks[(size_t)page * p.c.Hkv + kvh];
-                        vs = p.c.vs[(size_t)page * p.c.Hkv + kvh];
-                    }
-                }
-            }
+            kvh = w.rest / p.HT;
+            if (is8) tile = tile_of(p, s, w.b, kvh, w.off);
         }
         const uint32_t all = __ballot_sync(0xffffffffu, is8);
         for (uint32_t left = all; left; left &= left - 1, ++slot) {
@@ -274,9 +138,9 @@ __device__ __forceinline__ void load_run(const DecodeKv8Params& p, DecodeSmem& s
                 if (slot >= DK_STAGES && !mbar_wait(&sm.empty[st], (slot / DK_STAGES - 1) & 1, &sm.abort, DK_WAIT_RING))
                     ok = false;
                 if (ok) {
-                    sm.meta[st] = Meta{ks, vs, j, 0};
-                    if (page >= 0) {
-                        const int row = (page * p.c.Hkv + kvh) * kBlk;
+                    sm.meta[st] = Meta{tile.ks, tile.vs, tile.j, 0};
+                    if (tile.page >= 0) {
+                        const int row = (tile.page * p.c.Hkv + kvh) * kBlk;
                         mbar_expect_tx(&sm.full[st], 2 * kBlkBytes);
                         tma_load_2d(sm.k[st], &p.tm_k, &sm.full[st], 0, row);
                         tma_load_2d(sm.v[st], &p.tm_v, &sm.full[st], 0, row);
@@ -297,167 +161,6 @@ __device__ __forceinline__ void load_run(const DecodeKv8Params& p, DecodeSmem& s
 
 // ------------------------------------------------------------------ computing warps
 
-// A warp's share of an item.  Lane (r, c) = (lane / 4, lane % 4) holds head r: of O the dims 16 i + 4 c .. + 3
-// for i = 0 .. 7.
-struct State {
-    float m, l;      // running maximum (base 2), this lane's part of the sum (times 2^14)
-    float o[8][4];
-};
-
-// Scores of a set of keys in base 2 -> p relative to the set's own maximum (times 2^14: as fp16 down to 2^-38 of
-// it, whatever the sets before had), the running maximum and sum.  a: factor for O so far; b: for this set's.
-template <int N> __device__ __forceinline__ void soften(State& t, float (&s)[N], float& a, float& b) {
-    float mt = s[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mt = fmaxf(mt, s[i]);
-    mt = fmaxf(quad_max(mt), -3e38f);     // scores of -infinity alone have p = 0, not NaN
-    const float m = fmaxf(t.m, mt);
-    a = fast_exp2(t.m - m);               // 0 from the empty start
-    b = fast_exp2(mt - m);
-    const float base = mt - 14.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s[i] = fast_exp2(s[i] - base);
-        sum += s[i];
-    }
-    t.l = fmaf(t.l, a, sum * b);
-    t.m = m;
-}
-
-template <int CODE>
-__device__ __forceinline__ void block8(State& t, const uint32_t (&q)[8][2], float qscale, uint32_t k_addr, uint32_t v_addr,
-                                       const Meta& meta, int lo) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    const int mi = lane >> 3, r = lane & 7;            // ldmatrix: this lane's row r of matrix mi
-    float s[16];
-    // S: 8 keys at a time; matrices are the 16-byte chunks of the keys' rows
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t row = k_addr + (n * 8 + r) * kD;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w[4];
-            ldsm4(row + (((4 * half + mi) ^ r) << 4), w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t b0, b1;
-                halves4<CODE>(w[i], b0, b1);
-                mma16816<false>(d, q[4 * half + i][0], 0u, q[4 * half + i][1], 0u, b0, b1);
-            }
-        }
-        s[2 * n] = d[0];
-        s[2 * n + 1] = d[1];
-    }
-    const float f = meta.ks * qscale;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] *= f;
-    if (meta.j * kBlk < lo) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (meta.j * kBlk + (i >> 1) * 8 + 2 * c + (i & 1) < lo) s[i] = -INFINITY;
-    }
-    float a, b;
-    soften(t, s, a, b);
-    uint32_t hi[8], lo2[8];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) split2<false>(s[2 * n], s[2 * n + 1], hi[n], lo2[n]);
-    // O: 16 dims at a time (their 16-byte chunk); matrices are groups of 8 keys, transposed: a lane gets keys
-    // 2c, 2c+1 of the dims 2r, 2r+1 of the chunk
-    const float vs = meta.vs * (b * kInvP);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w[4], be[4], bo[4];
-            ldsm4t(v_addr + (32 * half + 8 * mi + r) * kD + ((i ^ r) << 4), w);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) halves4<CODE>(__byte_perm(w[x], 0, 0x3120), be[x], bo[x]);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int n = 4 * half + 2 * kk;
-                mma16816<false>(e, hi[n], lo2[n], hi[n + 1], lo2[n + 1], be[2 * kk], be[2 * kk + 1]);
-                mma16816<false>(o, hi[n], lo2[n], hi[n + 1], lo2[n + 1], bo[2 * kk], bo[2 * kk + 1]);
-            }
-        }
-        t.o[i][0] = fmaf(e[0] + e[2], vs, t.o[i][0] * a);
-        t.o[i][1] = fmaf(o[0] + o[2], vs, t.o[i][1] * a);
-        t.o[i][2] = fmaf(e[1] + e[3], vs, t.o[i][2] * a);
-        t.o[i][3] = fmaf(o[1] + o[3], vs, t.o[i][3] * a);
-    }
-}
-
-// 16 keys of the tail, k0 .. k0 + 15 of its block, valid where first <= key <= last; 16-bit products of the
-// types as they are (values in bf16 span more than fp16 does)
-template <typename TK>
-__device__ __forceinline__ void tail16(State& t, const uint32_t (&q)[8][2], float scale, const TK* k, const bf16* v, int k0,
-                                       int first, int last) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    uint2 kw[2][8];
-    uint32_t vw[8][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const TK* row = k + (k0 + 8 * n + r) * kD + 4 * c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) kw[n][i] = *reinterpret_cast<const uint2*>(row + 16 * i);
-    }
-    bool on[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int key = k0 + 2 * c + (x & 1) + 8 * (x >> 1);
-        on[x] = key >= first && key <= last;
-        // a masked row may hold anything: it must not reach the product
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            vw[i][x] = on[x] ? *reinterpret_cast<const uint32_t*>(v + key * kD + 16 * i + 2 * r) : 0u;
-    }
-    float s[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma16816<KeyType<TK>::kBf>(d, q[i][0], 0u, q[i][1], 0u, kw[n][i].x, kw[n][i].y);
-        s[2 * n] = on[2 * n] ? d[0] * scale : -INFINITY;
-        s[2 * n + 1] = on[2 * n + 1] ? d[1] * scale : -INFINITY;
-    }
-    float a, b;
-    soften(t, s, a, b);
-    b *= kInvP;
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) split2<true>(s[2 * n], s[2 * n + 1], hi[n], lo[n]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816<true>(e, hi[0], lo[0], hi[1], lo[1], __byte_perm(vw[i][0], vw[i][1], 0x5410),
-                       __byte_perm(vw[i][2], vw[i][3], 0x5410));
-        mma16816<true>(o, hi[0], lo[0], hi[1], lo[1], __byte_perm(vw[i][0], vw[i][1], 0x7632),
-                       __byte_perm(vw[i][2], vw[i][3], 0x7632));
-        t.o[i][0] = fmaf(e[0] + e[2], b, t.o[i][0] * a);
-        t.o[i][1] = fmaf(o[0] + o[2], b, t.o[i][1] * a);
-        t.o[i][2] = fmaf(e[1] + e[3], b, t.o[i][2] * a);
-        t.o[i][3] = fmaf(o[1] + o[3], b, t.o[i][3] * a);
-    }
-}
-
-// out and lse of four dims of one head from its maximum, sum and O
-__device__ __forceinline__ void finish4(const DecodeKv8Params& p, size_t head, int d, float m, float l, const float (&o)[4]) {
-    const float inv = 1.f / (l * kInvP);
-    float x[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    if (p.g) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p.g + head * kD + d);
-        const float2 a = unpack_bf16(w.x), b = unpack_bf16(w.y);
-        x[0] *= sigmoidf_(a.x);
-        x[1] *= sigmoidf_(a.y);
-        x[2] *= sigmoidf_(b.x);
-        x[3] *= sigmoidf_(b.y);
-    }
-    *reinterpret_cast<uint2*>(p.out + head * kD + d) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    if (d == 0) p.lse[head] = (m + log2f(l) - 14.f) * kLn2;
-}
-
 template <typename TK, int CODE>
 __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem& sm, const Run& run, long long lo,
                                             long long hi) {
@@ -477,56 +180,19 @@ __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem
         t.m = -INFINITY;
         t.l = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t.o[i][0] = t.o[i][1] = t.o[i][2] = t.o[i][3] = 0.f;
+        for (int i = 0; i < 8; ++i) t.e[i] = t.o[i] = make_float2(0.f, 0.f);
         if (s.idle || s.bad) {
-            if (warp == 0 && r < nh) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t u = s.idle ? 0u : 0x7fff7fffu;
-                    *reinterpret_cast<uint2*>(p.out + head * kD + 16 * i + 4 * c) = make_uint2(u, u);
-                }
-                if (c == 0) p.lse[head] = s.idle ? -INFINITY : NAN;
-            }
+            if (warp == 0 && r < nh) no_answer(p, head, s.idle);
         } else {
-            uint32_t q16[8][2];
-            float qs = p.scale_log2;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint2 u = make_uint2(0u, 0u);
-                if (r < nh) u = *reinterpret_cast<const uint2*>(static_cast<const TK*>(p.q) + head * kD + 16 * i + 4 * c);
-                q16[i][0] = u.x;
-                q16[i][1] = u.y;
-            }
-            uint32_t qt[8][2];   // as they are, for the tail
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                qt[i][0] = q16[i][0];
-                qt[i][1] = q16[i][1];
-            }
-            if (KeyType<TK>::kBf) {
-                float mx = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 a = unpack_bf16(q16[i][0]), b = unpack_bf16(q16[i][1]);
-                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
-                }
-                mx = quad_max(mx);
-                const int ex = min(254, 268 - (int)(__float_as_uint(mx) >> 23));
-                const float up = __uint_as_float((uint32_t)ex << 23);   // 2^14 / 2^floor(log2 mx)
-                qs = p.scale_log2 / up;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 a = unpack_bf16(q16[i][0]), b = unpack_bf16(q16[i][1]);
-                    q16[i][0] = pack_half(a.x * up, a.y * up);
-                    q16[i][1] = pack_half(b.x * up, b.y * up);
-                }
-            }
-            for (int i = (warp - slot) & 3; i < n8; i += DK_WARPS) {
+            uint32_t qt[8][2], q16[8][2];   // as they are, for the tail; as fp16, for codes
+            load_q<TK>(p, head, r < nh, qt);
+            const float qs = q_as_half<TK>(p, qt, q16);
+            for (int i = ((warp >> 1) - slot) & 1; i < n8; i += 2) {
                 const int sl = slot + i, st = sl % DK_STAGES;
                 if (mbar_wait(&sm.full[st], (sl / DK_STAGES) & 1, &sm.abort, DK_WAIT_LOAD)) {
                     const Meta meta = sm.meta[st];
                     if (meta.j >= 0)
-                        block8<CODE>(t, q16, qs, smem_u32(sm.k[st]), smem_u32(sm.v[st]), meta, s.lo);
+                        block8<CODE>(t, q16, qs, smem_u32(sm.k[st]), smem_u32(sm.v[st]), meta, s.lo, (warp & 1) * 32);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.empty[st]);
@@ -557,15 +223,17 @@ __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem
                 l = fmaf(sm.ml[i][r][1], fi, l);
                 if (i == warp) f = fi;
             }
+            const float2 ff = make_float2(f, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) t.o[i][e] *= f;
+            for (int i = 0; i < 8; ++i) {
+                t.e[i] = fmul2(t.e[i], ff);
+                t.o[i] = fmul2(t.o[i], ff);
+            }
             if (warp >= 2) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<float4*>(&sm.acc[warp - 2][r][16 * i + 4 * c]) =
-                        make_float4(t.o[i][0], t.o[i][1], t.o[i][2], t.o[i][3]);
+                        make_float4(t.e[i].x, t.o[i].x, t.e[i].y, t.o[i].y);
             }
             warps_sync();
             if (warp < 2) {
@@ -573,11 +241,9 @@ __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem
                 for (int i = 0; i < 8; ++i) {
                     float4* a = reinterpret_cast<float4*>(&sm.acc[warp][r][16 * i + 4 * c]);
                     const float4 y = *a;
-                    t.o[i][0] += y.x;
-                    t.o[i][1] += y.y;
-                    t.o[i][2] += y.z;
-                    t.o[i][3] += y.w;
-                    if (warp == 1) *a = make_float4(t.o[i][0], t.o[i][1], t.o[i][2], t.o[i][3]);
+                    t.e[i] = fadd2(t.e[i], make_float2(y.x, y.z));
+                    t.o[i] = fadd2(t.o[i], make_float2(y.y, y.w));
+                    if (warp == 1) *a = make_float4(t.e[i].x, t.o[i].x, t.e[i].y, t.o[i].y);
                 }
             }
             warps_sync();
@@ -588,7 +254,7 @@ __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 y = *reinterpret_cast<const float4*>(&sm.acc[1][r][16 * i + 4 * c]);
-                    const float o[4] = {t.o[i][0] + y.x, t.o[i][1] + y.y, t.o[i][2] + y.z, t.o[i][3] + y.w};
+                    const float o[4] = {t.e[i].x + y.x, t.o[i].x + y.y, t.e[i].y + y.z, t.o[i].y + y.w};
                     if (one)
                         finish4(p, head, 16 * i + 4 * c, m, l, o);
                     else
@@ -612,7 +278,7 @@ __global__ void __launch_bounds__(DK_THREADS, 2) kv8_decode_kernel(const __grid_
         if (lane == 0) {
             for (int i = 0; i < DK_STAGES; ++i) {
                 mbar_init(&sm.full[i], 1);
-                mbar_init(&sm.empty[i], 1);
+                mbar_init(&sm.empty[i], 2);
             }
             sm.abort = 0;
             fence_barrier_init();
@@ -799,6 +465,10 @@ int zgcm_attn_decode_kv8(const zgcm_kv8_cache* cache, const void* q, const void*
     if (!make_map(&p.tm_k, p.c.kc, p.c) || !make_map(&p.tm_v, p.c.vc, p.c)) return ZGCM_ERR_CUDA;
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     const bool f8 = p.c.code == ZGCM_E4M3;
+    // the most units of an item: a list's entries, or the blocks that a window can touch and the table hold
+    const long long touched = ((long long)window - 1 + kBlk - 1) / kBlk + 1;
+    if (kv8_direct_plan(p, blocks ? p.n_list + 1 : (int)(touched < p.c.NB ? touched : p.c.NB)))
+        return kv8_direct_launch(p, stream) == cudaSuccess ? ZGCM_OK : ZGCM_ERR_CUDA;
     const cudaError_t e = p.c.key == ZGCM_BF16
                               ? (f8 ? launch<bf16, ZGCM_E4M3>(p, stream) : launch<bf16, ZGCM_INT8>(p, stream))
                               : (f8 ? launch<__half, ZGCM_E4M3>(p, stream) : launch<__half, ZGCM_INT8>(p, stream));

@@ -1,0 +1,255 @@
+// kv8_direct.cu — decode attention over the 8-bit block cache in one launch, for items of few blocks (a sliding
+// layer's window, a list of selected blocks, short contexts): see kv8_decode.cu for the arithmetic and for the
+// kernel of long ones.
+//
+// There the whole call is a few microseconds, most of them latencies in a row: position, page number, codes.  So a
+// cluster of 1 to 8 CTAs takes an item whose units are split evenly among them; nothing but its own position
+// decides a CTA's work, the rows of q and of the tail load while page numbers do, the CTAs' parts meet in
+// shared memory across the cluster (each finishes a share of the dims), and there is no second kernel.  Four CTAs of
+// four warps fit on an SM: their latencies overlap.  Two warps share a block, 32 keys each; the
+// first of them also fetches the pair's page numbers, 32 blocks ahead, and keeps the pair's half of the ring full.
+#include <cooperative_groups.h>
+
+#include "kv8_attn.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace zgcm {
+namespace {
+
+constexpr int DD_THREADS = 128;
+constexpr int DD_MAX_STAGES = 4;
+constexpr int DD_WAIT_LOAD = 0x820, DD_WAIT_RING = 0x821;
+
+struct DirectSmem {
+    uint64_t full[DD_MAX_STAGES], empty[DD_MAX_STAGES];
+    Meta meta[DD_MAX_STAGES];
+    float ml[4][DK_HEADS][2];
+    float cta_ml[DK_HEADS][2];
+    int abort;
+};
+
+template <typename TK, int CODE>
+__global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_constant__ DecodeKv8Params p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ DirectSmem sm;
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    const int rank = blockIdx.x % p.split, item = blockIdx.x / p.split;
+    const int b = item / (p.c.Hkv * p.HT), rest = item % (p.c.Hkv * p.HT), kvh = rest / p.HT, ht = rest % p.HT;
+    const int nh = min(DK_HEADS, p.G - ht * DK_HEADS);
+    const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS;
+    const int pos = p.pos[b];
+    uint32_t qt[8][2];
+    load_q<TK>(p, head0 + r, r < nh, qt);
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&sm.full[i], 2);    // the codes' bytes, and the scales
+            mbar_init(&sm.empty[i], 2);   // the pair
+        }
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const Span s = span_of(p, pos);
+    if (s.idle || s.bad) {   // the same for the whole cluster
+        if (rank == 0 && warp == 0 && r < nh) no_answer(p, head0 + r, s.idle);
+        return;
+    }
+    // this CTA's blocks, and of them this pair's: every second one
+    const int n8 = s.units - 1, u0 = (int)((long long)n8 * rank / p.split), u1 = (int)((long long)n8 * (rank + 1) / p.split);
+    const int team = warp >> 1, per = p.stages / 2, nt = (u1 - u0 - team + 1) / 2;
+    unsigned char* base = ring + team * per * 2 * kBlkBytes;
+    uint64_t *full = sm.full + team * per, *empty = sm.empty + team * per;
+    Meta* meta = sm.meta + team * per;
+    const bool loads = (warp & 1) == 0;
+    Tile tile{-1, -1, 0.f, 0.f};
+    auto fetch = [&](int batch) {   // lane i: the pair's block 32 batch + i
+        const int k = 32 * batch + lane;
+        tile = Tile{-1, -1, 0.f, 0.f};
+        if (k < nt) tile = tile_of(p, s, b, kvh, u0 + team + 2 * k);
+    };
+    auto codes = [&](int k) {       // by the lane that holds block k
+        const int st = k % per;
+        if (tile.page >= 0) {
+            const int row = (tile.page * p.c.Hkv + kvh) * kBlk;
+            mbar_expect_tx(&full[st], 2 * kBlkBytes);
+            tma_load_2d(base + st * 2 * kBlkBytes, &p.tm_k, &full[st], 0, row);
+            tma_load_2d(base + st * 2 * kBlkBytes + kBlkBytes, &p.tm_v, &full[st], 0, row);
+        } else {
+            mbar_arrive(&full[st]);
+        }
+    };
+    auto scales = [&](int k) {
+        meta[k % per] = Meta{tile.ks, tile.vs, tile.j, 0};
+        mbar_arrive(&full[k % per]);
+    };
+    if (loads) {
+        fetch(0);
+        // all codes first: the scales are still on their way
+        if (lane < min(per, nt)) codes(lane);
+        if (lane < min(per, nt)) scales(lane);
+        __syncwarp();
+    }
+
+    State t;
+    t.m = -INFINITY;
+    t.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t.e[i] = t.o[i] = make_float2(0.f, 0.f);
+    if (rank == 0) {
+        const int last = pos - s.own * kBlk, first = s.lo - s.own * kBlk;
+        if (warp * 16 <= last && warp * 16 + 15 >= first) {
+            const size_t at = ((size_t)b * p.c.Hkv + kvh) * kBlkBytes;
+            tail16<TK>(t, qt, p.scale_log2, reinterpret_cast<const TK*>(p.c.ktail) + at, p.c.vtail + at, warp * 16, first, last);
+        }
+    }
+    uint32_t q16[8][2];
+    const float qs = q_as_half<TK>(p, qt, q16);
+    bool ok = true;
+    int issued = min(per, nt);
+    for (int k = 0; k < nt; ++k) {
+        const int st = k % per, phase = (k / per) & 1;
+        if (ok && mbar_wait(&full[st], phase, &sm.abort, DD_WAIT_LOAD)) {
+            const Meta m = meta[st];
+            if (m.j >= 0)
+                block8<CODE>(t, q16, qs, smem_u32(base + st * 2 * kBlkBytes), smem_u32(base + st * 2 * kBlkBytes + kBlkBytes), m,
+                             s.lo, (warp & 1) * 32);
+        } else {
+            ok = false;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        const int next = k + per;
+        if (loads && next < nt) {
+            if (next % 32 == 0) fetch(next / 32);
+            if (ok && lane == next % 32) {
+                if (mbar_wait(&empty[st], phase, &sm.abort, DD_WAIT_RING)) {
+                    codes(next);
+                    scales(next);
+                } else {
+                    ok = false;
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) ++issued;
+        }
+    }
+    // a wait that expired leaves copies in flight: not past them
+    if (loads && !ok)
+        for (int k = max(0, issued - per); k < issued; ++k) mbar_wait_drain(&full[k % per], (k / per) & 1);
+
+    // the warps' parts, in a fixed order; the ring is free once all have come here
+    float(*acc)[DK_HEADS][kD] = reinterpret_cast<float(*)[DK_HEADS][kD]>(ring);                      // [warp]
+    float(*sum)[kD] = reinterpret_cast<float(*)[kD]>(ring + 4 * DK_HEADS * kD * sizeof(float));      // the CTA's
+    t.l += __shfl_xor_sync(0xffffffffu, t.l, 1);
+    t.l += __shfl_xor_sync(0xffffffffu, t.l, 2);
+    if (c == 0) {
+        sm.ml[warp][r][0] = t.m;
+        sm.ml[warp][r][1] = t.l;
+    }
+    __syncthreads();
+    float m = -INFINITY, l = 0.f, f = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, sm.ml[i][r][0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a part without keys counts nothing; one whose scores were all NaN has a NaN sum
+        const float fi = sm.ml[i][r][1] == 0.f ? 0.f : fast_exp2(sm.ml[i][r][0] - m);
+        l = fmaf(sm.ml[i][r][1], fi, l);
+        if (i == warp) f = fi;
+    }
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 x = fmul2(t.e[i], f2), y = fmul2(t.o[i], f2);
+        *reinterpret_cast<float4*>(&acc[warp][r][16 * i + 4 * c]) = make_float4(x.x, y.x, x.y, y.y);
+    }
+    if (warp == 0 && c == 0) {
+        sm.cta_ml[r][0] = m;
+        sm.cta_ml[r][1] = l;
+    }
+    __syncthreads();
+    // 256 places of a head and 4 dims
+    float4 mine[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int h = (tid + DD_THREADS * i) >> 5, d = 4 * (tid & 31);
+        mine[i] = *reinterpret_cast<const float4*>(&acc[0][h][d]);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(&acc[w][h][d]);
+            mine[i].x += y.x;
+            mine[i].y += y.y;
+            mine[i].z += y.z;
+            mine[i].w += y.w;
+        }
+        if (p.split == 1) {
+            const float o[4] = {mine[i].x, mine[i].y, mine[i].z, mine[i].w};
+            if (h < nh) finish4(p, head0 + h, d, sm.cta_ml[h][0], sm.cta_ml[h][1], o);
+        } else {
+            *reinterpret_cast<float4*>(&sum[h][d]) = mine[i];
+        }
+    }
+    if (p.split > 1) {
+        cluster.sync();
+        const int share = 256 / p.split;   // at most one place of a thread
+        const int at = rank * share + tid, h = at >> 5, d = 4 * (at & 31);
+        if (tid < share && h < nh) {
+            float mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < p.split; ++i) mm = fmaxf(mm, cluster.map_shared_rank(&sm, i)->cta_ml[h][0]);
+            for (int i = 0; i < p.split; ++i) {
+                const float* ml = cluster.map_shared_rank(&sm, i)->cta_ml[h];
+                const float4 y = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sum[h][d], i));
+                const float fi = ml[1] == 0.f ? 0.f : fast_exp2(ml[0] - mm);
+                ll = fmaf(ml[1], fi, ll);
+                o[0] = fmaf(y.x, fi, o[0]);
+                o[1] = fmaf(y.y, fi, o[1]);
+                o[2] = fmaf(y.z, fi, o[2]);
+                o[3] = fmaf(y.w, fi, o[3]);
+            }
+            finish4(p, head0 + h, d, mm, ll, o);
+        }
+        cluster.sync();   // shared memory that others read stays
+    }
+    if (tid == 0 && sm.abort) *p.err = sm.abort;
+}
+
+template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
+    const size_t smem = (size_t)p.stages * 2 * kBlkBytes + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         DD_MAX_STAGES * 2 * kBlkBytes + 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * p.HT * p.split));
+    cfg.blockDim = dim3(DD_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_direct_kernel<TK, CODE>, p);
+}
+
+}  // namespace
+
+// Whether this kernel takes the call, and how an item is split.  units: the most an item can have.
+bool kv8_direct_plan(DecodeKv8Params& p, int units) {
+    const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
+    p.split = 1;
+    while (p.split < 8 && items * p.split * 2 <= 592 && units > 2 * p.split) p.split *= 2;
+    p.stages = items * p.split <= 296 && units > 4 * p.split ? 4 : 2;
+    return units <= 64 * p.split && items * p.split <= 0x7fffffffLL;
+}
+
+cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream) {
+    const bool f8 = p.c.code == ZGCM_E4M3;
+    return p.c.key == ZGCM_BF16 ? (f8 ? launch<bf16, ZGCM_E4M3>(p, stream) : launch<bf16, ZGCM_INT8>(p, stream))
+                                : (f8 ? launch<__half, ZGCM_E4M3>(p, stream) : launch<__half, ZGCM_INT8>(p, stream));
+}
+
+}  // namespace zgcm

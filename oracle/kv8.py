@@ -52,7 +52,7 @@ def stored(x, code):
 def attend(q, g, k, v, *, code, window, scale=None, blocks=None):
     """The newest token's attention: q, g [Hq, D] (g may be None), k, v [S, Hkv, D] its
     sequence's tokens.  blocks: per KV head the earlier blocks to read.  Returns out [Hq, D], lse [Hq]
-    and, for tolerances, the sums of |p v| [Hq, D] and the sums over blocks of their largest p times
+    and, for tolerances, the sums of |p v| [Hq, D] and the sums over blocks of their p times
     their largest |v| [Hq]."""
     q, kk, vv = _f64(q), stored(k, code), stored(v, code)
     S, Hkv, D = kk.shape
@@ -73,7 +73,8 @@ def attend(q, g, k, v, *, code, window, scale=None, blocks=None):
         out[h] = w @ vv[seen, kv]
         mag[h] = w @ np.abs(vv[seen, kv])
         at = np.flatnonzero(seen) // BLOCK
-        top[h] = sum(w[at == j].max() * np.abs(vv[seen, kv][at == j]).max() for j in np.unique(at))
+        starts = np.flatnonzero(np.r_[True, at[1:] != at[:-1]])
+        top[h] = (np.add.reduceat(w, starts) * np.maximum.reduceat(np.abs(vv[seen, kv]).max(1), starts)).sum()
     if g is not None:
         sg = 1.0 / (1.0 + np.exp(-_f64(g)))
         out, mag, top = out * sg, mag * sg, top * sg.max(1)

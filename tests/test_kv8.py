@@ -10,7 +10,7 @@ and its 16-bit halves 2^-20; a score's rounding in base 2 adds 2^-24 |s|, covere
 bound; sums of up to 2^16 keys in tiles and partial records 2^-17.  The output is then rounded once
 to bf16 (2^-8 of the value): 2^-8 |ref| + (2 e + 2^-15) sum p |v|.  lse: e + 2^-17 + 2^-22 |lse|.
 A probability enters the second product as two fp16 halves of p 2^14 relative to its block's largest: off by half
-their smallest step, 2^-25 / 2^14 = 2^-39 of that, for each of 64 keys: 2^-33 of the block's largest p times its
+their smallest step, 2^-25 / 2^14 = 2^-39 of that, for each of 64 keys: 2^-33 of the block's p times its
 largest |v| (2^-15 sum p |v| covers the rest, 2^-22 relative).
 Selected blocks: equal.
 """
@@ -372,6 +372,36 @@ def test_decode_lengths(cuda, code, key):
     _check_decode(c, k, v, q, g, code, lens=lens)
     for window in (1, 64, 65, 128, 700):
         _check_decode(c, k, v, q, g, code, lens=lens, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("code,key", [("e4m3", "fp16"), ("int8", "bf16")])
+@pytest.mark.parametrize("B,Hq,Hkv,longest", [(1, 4, 1, 40000), (3, 12, 1, 36000), (90, 8, 2, 4700), (300, 1, 1, 4500)])
+def test_decode_long_and_many(cuda, code, key, B, Hq, Hkv, longest):
+    """Contexts of hundreds of blocks, and more sequences than an SM count: runs that begin and end inside
+    sequences, short ones among long ones, idle ones."""
+    g0 = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, longest + 1, (B,), generator=g0).tolist()
+    lens[0] = longest
+    for b in range(3, B, 7):
+        lens[b] = (0, 1, 64, 65, 130)[b % 5]
+    k, v = _tokens(min(B, 4), longest, Hkv, key, seed=B)
+    src = [b % 4 for b in range(B)]
+    c = _new(B, longest // 64 + 1, Hkv, code, key)
+    ga.zgcm_kv8_append(c, k.cuda()[src], v.cuda()[src], _i32(*[0] * B), count=_i32(*lens))
+    q, g = _queries(B, Hq, key)
+    pos = _i32(*[n - 1 for n in lens])
+    out, lse = ga.zgcm_attn_decode_kv8(c, q.cuda(), g.cuda(), pos, window=ALL)
+    again = ga.zgcm_attn_decode_kv8(c, q.cuda(), g.cuda(), pos, window=ALL)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    for b in sorted({0, 1, 2, 3, 10, 17, B // 2, B - 2, B - 1} & set(range(B))):
+        if lens[b] == 0:
+            assert not out[b].any() and torch.isneginf(lse[b]).all()
+            continue
+        x, y = k[src[b], :lens[b]], v[src[b], :lens[b]]
+        _close((b, lens[b]), out[b], lse[b], *kv8.attend(q[b], g[b], x, y, code=code, window=ALL), q[b], x, 128 ** -0.5)
+    assert torch.isfinite(out).all()
+    assert ga.zgcm_attn_device_error() == 0
 
 
 @gpu
