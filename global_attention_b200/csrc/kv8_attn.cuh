@@ -14,7 +14,7 @@ constexpr int DK_HEADS = 8;                // heads of an item
 constexpr float kInvP = 1.f / 16384.f;     // p is held times 2^14: as fp16 above its subnormals
 
 struct DecodeKv8Params {
-    CUtensorMap tm_k, tm_v;                // [n_pages * Hkv * 64, 128] bytes, box 64 rows
+    CUtensorMap tm_k, tm_v;                // [n_pages * Hkv * 64, 128] bytes, box 32 rows
     Kv8 c;
     const void* q;
     const bf16* g;
@@ -22,7 +22,7 @@ struct DecodeKv8Params {
     const int* blocks;
     int n_list, Hq, G, HT, W;              // HT: items of a KV head (8 heads each)
     int rows;                              // heads a record has room for: min(G, 8)
-    int split, stages;                     // kv8_direct_kernel: CTAs of an item, stages of its ring
+    int split;                             // kv8_direct_kernel: CTAs of an item
     float scale_log2;
     bf16* out;
     float* lse;
@@ -47,12 +47,6 @@ __device__ __forceinline__ Span span_of(const DecodeKv8Params& p, int pos) {
     s.units = s.idle || s.bad ? 1 : (p.blocks ? p.n_list : s.own - s.jlo) + 1;
     return s;
 }
-
-struct Meta {
-    float ks, vs;
-    int j;        // block, or -1: passed over
-    int pad;
-};
 
 // ------------------------------------------------------------------ tensor-core and code helpers
 
@@ -139,47 +133,59 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// a pair of values as a 16-bit pair and the pair of what the rounding left
-template <bool BF> __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    if (BF) {
-        hi = pack_bf16(a, b);
-        const float2 r = unpack_bf16(hi);
-        lo = pack_bf16(a - r.x, b - r.y);
-    } else {
-        hi = pack_half(a, b);
-        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        lo = pack_half(a - r.x, b - r.y);
-    }
+// an 8 x 8 matrix of 16-bit values (two a lane) transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
+// over the 8 lanes of a column: those with the same lane % 4
+__device__ __forceinline__ float column_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float column_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
 __device__ __forceinline__ float quad_max(float x) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-// A warp's share of an item.  Lane (r, c) = (lane / 4, lane % 4) holds head r: of O, for i = 0 .. 7, the dims
-// 16 i + 4 c + {0, 2} in e[i] and + {1, 3} in o[i] (the pairs a product leaves side by side).
+
+// A warp's share of an item.  Lane (r, c) = (lane / 4, lane % 4) holds the heads 2 c and 2 c + 1 (.x and .y): of O, for
+// i = 0 .. 7, the dims 16 i + 2 r in o[i][0] and 16 i + 2 r + 1 in o[i][1].
 struct State {
-    float m, l;      // running maximum (base 2), this lane's part of the sum (times 2^14)
-    float2 e[8], o[8];
+    float2 m, l;      // running maximum (base 2), this lane's part of the sum (times 2^14)
+    float2 o[8][2];
+    __device__ __forceinline__ State() : m(make_float2(-INFINITY, -INFINITY)), l(make_float2(0.f, 0.f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
+    }
 };
 
-// O of one 16-dim chunk <- O a + (its two rows: of p rounded and of what the rounding left) f
-__device__ __forceinline__ void join_o(State& t, int i, const float (&e)[4], const float (&o)[4], float2 a, float2 f) {
-    t.e[i] = ffma2(fadd2(make_float2(e[0], e[1]), make_float2(e[2], e[3])), f, fmul2(t.e[i], a));
-    t.o[i] = ffma2(fadd2(make_float2(o[0], o[1]), make_float2(o[2], o[3])), f, fmul2(t.o[i], a));
+// O of one 16-dim chunk <- O a + d f
+__device__ __forceinline__ void join_o(State& t, int i, const float (&d)[4], float2 a, float2 f) {
+    t.o[i][0] = ffma2(make_float2(d[0], d[1]), f, fmul2(t.o[i][0], a));
+    t.o[i][1] = ffma2(make_float2(d[2], d[3]), f, fmul2(t.o[i][1], a));
 }
 
-// Scores of a set of keys in base 2 -> p relative to the set's own maximum (times 2^14: as fp16 down to 2^-38 of
-// it, whatever the sets before had), the running maximum and sum.  a: factor for O so far; b: for this set's.
-template <int N> __device__ __forceinline__ void soften(State& t, float2 (&s)[N], float& a, float& b) {
-    float mt = fmaxf(s[0].x, s[0].y);
+// Scores of a set of keys in base 2 (N of this lane's two heads) -> p relative to the set's own maximum (times 2^14: as
+// fp16 down to 2^-38 of it, whatever the sets before had), the running maximum and sum.  a: factor for O so far; b: for
+// this set's.
+template <int N> __device__ __forceinline__ void soften(State& t, float2 (&s)[N], float2& a, float2& b) {
+    float2 mt = s[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) mt = fmaxf(mt, fmaxf(s[i].x, s[i].y));
-    mt = fmaxf(quad_max(mt), -3e38f);     // scores of -infinity alone have p = 0, not NaN
-    const float m = fmaxf(t.m, mt);
-    a = fast_exp2(t.m - m);               // 0 from the empty start
-    b = fast_exp2(mt - m);
-    const float2 base = make_float2(14.f - mt, 14.f - mt);
+    for (int i = 1; i < N; ++i) mt = make_float2(fmaxf(mt.x, s[i].x), fmaxf(mt.y, s[i].y));
+    mt.x = fmaxf(column_max(mt.x), -3e38f);     // scores of -infinity alone have p = 0, not NaN
+    mt.y = fmaxf(column_max(mt.y), -3e38f);
+    const float2 m = make_float2(fmaxf(t.m.x, mt.x), fmaxf(t.m.y, mt.y));
+    a = make_float2(fast_exp2(t.m.x - m.x), fast_exp2(t.m.y - m.y));   // 0 from the empty start
+    b = make_float2(fast_exp2(mt.x - m.x), fast_exp2(mt.y - m.y));
+    const float2 base = make_float2(14.f - mt.x, 14.f - mt.y);
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -187,75 +193,63 @@ template <int N> __device__ __forceinline__ void soften(State& t, float2 (&s)[N]
         s[i] = make_float2(fast_exp2(s[i].x), fast_exp2(s[i].y));
         sum = fadd2(sum, s[i]);
     }
-    t.l = fmaf(t.l, a, (sum.x + sum.y) * b);
+    t.l = ffma2(t.l, a, fmul2(sum, b));
     t.m = m;
 }
 
-// 32 keys of a block, those from k0
+// Scores in base 2 of 32 keys at k_addr, of whose block the first `masked` are before the window: s[2 i], s[2 i + 1] of
+// the keys 16 i + r and 16 i + 8 + r.
 template <int CODE>
-__device__ __forceinline__ void block8(State& t, const uint32_t (&q)[8][2], float qscale, uint32_t k_addr, uint32_t v_addr,
-                                       const Meta& meta, int lo, int k0) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    const int mi = lane >> 3, r = lane & 7;            // ldmatrix: this lane's row r of matrix mi
-    float2 s[4];
-    k_addr += k0 * kD;
-    v_addr += k0 * kD;
-    // S: 8 keys at a time; matrices are the 16-byte chunks of the keys' rows
-    const float2 f = make_float2(meta.ks * qscale, meta.ks * qscale);
+__device__ __forceinline__ void scores32(float2 (&s)[4], const uint32_t (&q)[8][2], float2 f, uint32_t k_addr, int masked) {
+    const int lane = threadIdx.x & 31, r = lane >> 2;
+    // ldmatrix: this lane's row of matrix mi; matrices are 8 keys (mi & 1) of a 16-byte chunk (mi >> 1)
+    const int mi = lane >> 3, row = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int t = 0; t < 2; ++t) {
         float d[4];
-        const uint32_t row = k_addr + (n * 8 + r) * kD;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w[4];
-            ldsm4(row + (((4 * half + mi) ^ r) << 4), w);
+        for (int i = 0; i < 8; i += 2) {
+            uint32_t w[4], x[4], y[4];
+            ldsm4(k_addr + (16 * t + row) * kD + (((i + (mi >> 1)) ^ (lane & 7)) << 4), w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t b0, b1;
-                pairs_near<CODE>(w[i], b0, b1);
-                if (half + i == 0)
-                    mma16816<false>(d, q[0][0], 0u, q[0][1], 0u, b0, b1, 0.f, 0.f, 0.f, 0.f);
-                else
-                    mma16816<false>(d, q[4 * half + i][0], 0u, q[4 * half + i][1], 0u, b0, b1);
-            }
+            for (int j = 0; j < 4; ++j) pairs_near<CODE>(w[j], x[j], y[j]);
+            if (i == 0)
+                mma16816<false>(d, x[0], x[1], y[0], y[1], q[0][0], q[0][1], 0.f, 0.f, 0.f, 0.f);
+            else
+                mma16816<false>(d, x[0], x[1], y[0], y[1], q[i][0], q[i][1]);
+            mma16816<false>(d, x[2], x[3], y[2], y[3], q[i + 1][0], q[i + 1][1]);
         }
-        s[n] = fmul2(make_float2(d[0], d[1]), f);
+        s[2 * t] = fmul2(make_float2(d[0], d[1]), f);
+        s[2 * t + 1] = fmul2(make_float2(d[2], d[3]), f);
     }
-    if (meta.j * kBlk + k0 < lo) {
-        const int first = lo - meta.j * kBlk - k0 - 2 * c;
+    if (masked > 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (8 * n < first) s[n].x = -INFINITY;
-            if (8 * n + 1 < first) s[n].y = -INFINITY;
-        }
+        for (int i = 0; i < 4; ++i)
+            if (8 * i + r < masked) s[i] = make_float2(-INFINITY, -INFINITY);
     }
-    float a, b;
-    soften(t, s, a, b);
-    uint32_t hi[4], lo2[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) split2<false>(s[n].x, s[n].y, hi[n], lo2[n]);
-    // O: 16 dims at a time (their 16-byte chunk); matrices are groups of 8 keys, transposed: a lane gets keys
-    // 2c, 2c+1 of the dims 2r, 2r+1 of the chunk
-    const float vs = meta.vs * (b * kInvP);
-    const float2 a2 = make_float2(a, a), f2 = make_float2(vs, vs);
+}
+
+// O takes in 32 keys: b fragments of their p (two of each 16 keys), their values at v_addr.
+template <int CODE>
+__device__ __forceinline__ void values32(State& t, const uint32_t (&pb)[4], float2 a, float2 f, uint32_t v_addr) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3, r = lane & 7;
+    // 16 dims at a time (their 16-byte chunk); matrices are groups of 8 keys, transposed: a lane gets keys
+    // 2 c, 2 c + 1 of the dims 2 r, 2 r + 1 of the chunk (rows r and r + 8 of the product)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float e[4], o[4];
-        uint32_t w[4], be[4], bo[4];
+        float d[4];
+        uint32_t w[4], x[4], y[4];
         ldsm4t(v_addr + (8 * mi + r) * kD + ((i ^ r) << 4), w);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) pairs_apart<CODE>(w[x], be[x], bo[x]);
-        mma16816<false>(e, hi[0], lo2[0], hi[1], lo2[1], be[0], be[1], 0.f, 0.f, 0.f, 0.f);
-        mma16816<false>(o, hi[0], lo2[0], hi[1], lo2[1], bo[0], bo[1], 0.f, 0.f, 0.f, 0.f);
-        mma16816<false>(e, hi[2], lo2[2], hi[3], lo2[3], be[2], be[3]);
-        mma16816<false>(o, hi[2], lo2[2], hi[3], lo2[3], bo[2], bo[3]);
-        join_o(t, i, e, o, a2, f2);
+        for (int j = 0; j < 4; ++j) pairs_apart<CODE>(w[j], x[j], y[j]);
+        mma16816<false>(d, x[0], y[0], x[1], y[1], pb[0], pb[1], 0.f, 0.f, 0.f, 0.f);
+        mma16816<false>(d, x[2], y[2], x[3], y[3], pb[2], pb[3]);
+        join_o(t, i, d, a, f);
     }
 }
 
 // 16 keys of the tail, k0 .. k0 + 15 of its block, valid where first <= key <= last; 16-bit products of the
-// types as they are (values in bf16 span more than fp16 does)
+// types as they are (values in bf16 span more than fp16 does, so p goes in as two bf16, 16 bits of it)
 template <typename TK>
 __device__ __forceinline__ void tail16(State& t, const uint32_t (&q)[8][2], float scale, const TK* k, const bf16* v, int k0,
                                        int first, int last) {
@@ -268,40 +262,72 @@ __device__ __forceinline__ void tail16(State& t, const uint32_t (&q)[8][2], floa
 #pragma unroll
         for (int i = 0; i < 8; ++i) kw[n][i] = *reinterpret_cast<const uint2*>(row + 16 * i);
     }
-    bool on[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int key = k0 + 2 * c + (x & 1) + 8 * (x >> 1);
-        on[x] = key >= first && key <= last;
+        const bool on = key >= first && key <= last;
         // a masked row may hold anything: it must not reach the product
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            vw[i][x] = on[x] ? *reinterpret_cast<const uint32_t*>(v + key * kD + 16 * i + 2 * r) : 0u;
+        for (int i = 0; i < 8; ++i) vw[i][x] = on ? *reinterpret_cast<const uint32_t*>(v + key * kD + 16 * i + 2 * r) : 0u;
     }
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        mma16816<KeyType<TK>::kBf>(d, kw[0][i].x, kw[1][i].x, kw[0][i].y, kw[1][i].y, q[i][0], q[i][1]);
     float2 s[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma16816<KeyType<TK>::kBf>(d, q[i][0], 0u, q[i][1], 0u, kw[n][i].x, kw[n][i].y);
-        s[n].x = on[2 * n] ? d[0] * scale : -INFINITY;
-        s[n].y = on[2 * n + 1] ? d[1] * scale : -INFINITY;
+        const int key = k0 + 8 * n + r;
+        const bool on = key >= first && key <= last;
+        s[n] = on ? make_float2(d[2 * n] * scale, d[2 * n + 1] * scale) : make_float2(-INFINITY, -INFINITY);
     }
-    float a, b;
+    float2 a, b;
     soften(t, s, a, b);
-    b *= kInvP;
+    b = fmul2(b, make_float2(kInvP, kInvP));
     uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) split2<true>(s[n].x, s[n].y, hi[n], lo[n]);
+    for (int n = 0; n < 2; ++n) {
+        hi[n] = pack_bf16(s[n].x, s[n].y);
+        const float2 x = unpack_bf16(hi[n]);
+        lo[n] = transpose8(pack_bf16(s[n].x - x.x, s[n].y - x.y));
+        hi[n] = transpose8(hi[n]);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float e[4], o[4];
-        mma16816<true>(e, hi[0], lo[0], hi[1], lo[1], __byte_perm(vw[i][0], vw[i][1], 0x5410),
-                       __byte_perm(vw[i][2], vw[i][3], 0x5410), 0.f, 0.f, 0.f, 0.f);
-        mma16816<true>(o, hi[0], lo[0], hi[1], lo[1], __byte_perm(vw[i][0], vw[i][1], 0x7632),
-                       __byte_perm(vw[i][2], vw[i][3], 0x7632), 0.f, 0.f, 0.f, 0.f);
-        join_o(t, i, e, o, make_float2(a, a), make_float2(b, b));
+        float e[4];
+        const uint32_t a0 = __byte_perm(vw[i][0], vw[i][1], 0x5410), a1 = __byte_perm(vw[i][0], vw[i][1], 0x7632);
+        const uint32_t a2 = __byte_perm(vw[i][2], vw[i][3], 0x5410), a3 = __byte_perm(vw[i][2], vw[i][3], 0x7632);
+        mma16816<true>(e, a0, a1, a2, a3, hi[0], hi[1], 0.f, 0.f, 0.f, 0.f);
+        mma16816<true>(e, a0, a1, a2, a3, lo[0], lo[1]);
+        join_o(t, i, e, a, b);
     }
+}
+
+// Where a warp's maximum and sum go, [head]; every lane of the warp calls it.
+__device__ __forceinline__ void put_ml(const State& t, float (*ml)[2]) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    const float lx = column_sum(t.l.x), ly = column_sum(t.l.y);
+    if (lane < 4) {
+        *reinterpret_cast<float2*>(ml[2 * c]) = make_float2(t.m.x, lx);
+        *reinterpret_cast<float2*>(ml[2 * c + 1]) = make_float2(t.m.y, ly);
+    }
+}
+
+// The maximum and sum of four warps' parts of head h, and the factor of warp w's
+__device__ __forceinline__ float join_ml(const float (*ml)[DK_HEADS][2], int h, int w, float& m, float& l) {
+    float f = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[i][h][0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a part without keys counts nothing; one whose scores were all NaN has a NaN sum
+        const float fi = ml[i][h][1] == 0.f ? 0.f : fast_exp2(ml[i][h][0] - m);
+        l = fmaf(ml[i][h][1], fi, l);
+        if (i == w) f = fi;
+    }
+    return f;
 }
 
 // out and lse of four dims of one head from its maximum, sum and O
@@ -334,10 +360,10 @@ __device__ __forceinline__ void load_q(const DecodeKv8Params& p, size_t head, bo
     }
 }
 
-// q as the fp16 that meets codes, and the scale of its scores in base 2: fp16 as it is, bf16 times the power of
-// two that brings the head's largest element to 2^14
+// q as the fp16 that meets codes, and the scales of the scores of this lane's two heads in base 2: fp16 as it is, bf16
+// times the power of two that brings the head's largest element to 2^14
 template <typename TK>
-__device__ __forceinline__ float q_as_half(const DecodeKv8Params& p, const uint32_t (&q)[8][2], uint32_t (&h)[8][2]) {
+__device__ __forceinline__ float2 q_as_half(const DecodeKv8Params& p, const uint32_t (&q)[8][2], uint32_t (&h)[8][2]) {
     float mx = 0.f;
     if (KeyType<TK>::kBf) {
 #pragma unroll
@@ -359,7 +385,10 @@ __device__ __forceinline__ float q_as_half(const DecodeKv8Params& p, const uint3
             h[i][1] = pack_half(b.x * up, b.y * up);
         }
     }
-    return KeyType<TK>::kBf ? p.scale_log2 / up : p.scale_log2;
+    if (!KeyType<TK>::kBf) return make_float2(p.scale_log2, p.scale_log2);
+    const float qs = p.scale_log2 / up;   // of head r; this lane needs those of 2 c and 2 c + 1
+    const int c = threadIdx.x & 3;
+    return make_float2(__shfl_sync(0xffffffffu, qs, 8 * c), __shfl_sync(0xffffffffu, qs, 8 * c + 4));
 }
 
 // One sequence's row without an answer: zeros and -inf for an idle sequence, NaN for a window beyond the table.  By one
@@ -372,28 +401,132 @@ __device__ __forceinline__ void no_answer(const DecodeKv8Params& p, size_t head,
     if (c == 0) p.lse[head] = idle ? -INFINITY : NAN;
 }
 
-// Block number `i` of an item's units as the kernel reads it: block j (-1: passed over), page (-1: none), scales.
-struct Tile {
-    int j, page;
+// ------------------------------------------------------------------ a warp's stream of half blocks
+//
+// Two warps share a block, 32 keys each, and every warp feeds itself: lane i of it looks up the warp's block 32 n + i
+// (page, scales), 32 blocks ahead, and starts its copies when their turn comes, keys and values by turns into a ring
+// of 3 x 4 KB.  While keys are worked on their values and the next keys are on their way.
+
+constexpr int kHalfKeys = kBlk / 2;
+constexpr uint32_t kSlot = kHalfKeys * kD;      // bytes
+constexpr int kSlots = 3;
+
+struct Block {       // as the lane that holds it knows it
+    int j, row;      // block (-1: passed over); first of its rows in the codes (-1: no page)
     float ks, vs;
 };
 
-__device__ __forceinline__ Tile tile_of(const DecodeKv8Params& p, const Span& s, int b, int kvh, int i) {
-    Tile t{s.jlo + i, -1, 0.f, 0.f};
+// Block number `i` of an item's 8-bit units
+__device__ __forceinline__ Block block_of(const DecodeKv8Params& p, const Span& s, int b, int kvh, int i) {
+    Block t{s.jlo + i, -1, 0.f, 0.f};
     if (p.blocks) {
         const int* list = p.blocks + ((size_t)b * p.c.Hkv + kvh) * p.n_list + i;
         t.j = *list;
         if (t.j < s.jlo || t.j >= s.own || (i > 0 && t.j <= list[-1])) t.j = -1;
     }
     if (t.j >= 0) {
-        t.page = kv8_page(p.c, b, t.j);
+        const int page = kv8_page(p.c, b, t.j);
         t.ks = t.vs = NAN;          // a bad page reads as NaN
-        if (t.page >= 0) {
-            t.ks = p.c.ks[(size_t)t.page * p.c.Hkv + kvh];
-            t.vs = p.c.vs[(size_t)t.page * p.c.Hkv + kvh];
+        if (page >= 0) {
+            const int at = page * p.c.Hkv + kvh;
+            t.row = at * kBlk;
+            t.ks = p.c.ks[at];
+            t.vs = p.c.vs[at];
         }
     }
     return t;
 }
+
+struct WarpSmem {
+    uint64_t full[kSlots];
+    uint64_t pad;
+    Block block[4];        // of the warp's blocks n, n + 1, n + 2
+};
+
+struct Stream {
+    const DecodeKv8Params& p;
+    WarpSmem& sm;
+    unsigned char* ring;       // this warp's kSlots slots
+    volatile int* abort;
+    Block mine;                // of this lane, in the current 32
+    bool ok;
+
+    __device__ __forceinline__ Stream(const DecodeKv8Params& p_, WarpSmem& sm_, unsigned char* ring_, volatile int* abort_)
+        : p(p_), sm(sm_), ring(ring_), abort(abort_), mine{-1, -1, 0.f, 0.f}, ok(true) {}
+
+    // copy number c of the warp (keys of block c / 2 if even, else its values): by the lane that holds the block
+    __device__ __forceinline__ void copy(int c) {
+        if ((int)(threadIdx.x & 31) == ((c >> 1) & 31)) {
+            uint64_t* bar = &sm.full[c % kSlots];
+            if (mine.row >= 0) {
+                mbar_expect_tx(bar, kSlot);
+                tma_load_2d(ring + (c % kSlots) * kSlot, (c & 1) ? &p.tm_v : &p.tm_k, bar, 0,
+                            mine.row + ((threadIdx.x >> 5) & 1) * kHalfKeys);
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+    }
+    __device__ __forceinline__ void note(int n) {   // block n's numbers for the warp
+        if ((int)(threadIdx.x & 31) == (n & 31)) sm.block[n & 3] = mine;
+    }
+    // the first blocks are looked up: the first copies, then (they are still on their way) the scales
+    __device__ __forceinline__ void start(int blocks) {
+        if (blocks > 0) {
+            copy(0);
+            copy(1);
+        }
+        if (blocks > 1) copy(2);
+        if (blocks > 0) note(0);
+        if (blocks > 1) note(1);
+        __syncwarp();
+    }
+    // the slot of copy c has been read: what is next in it may come
+    __device__ __forceinline__ void reuse(int next, int copies) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && next < copies) copy(next);
+    }
+    __device__ __forceinline__ bool wait(int c, int where) {
+        if (ok) ok = mbar_wait(&sm.full[c % kSlots], (c / kSlots) & 1, abort, where);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+    }
+    // Block n of `blocks`; qs: the scales of this lane's two heads' scores.  fetch(i): looks the 32 blocks from 32 i up.
+    template <int CODE, typename Fetch>
+    __device__ __forceinline__ void take(State& t, const uint32_t (&q)[8][2], float2 qs, int lo, int n, int blocks, int where,
+                                         const Fetch& fetch) {
+        const uint32_t base = smem_u32(ring);
+        const bool here = wait(2 * n, where);
+        const Block k = sm.block[n & 3];
+        const bool on = here && k.j >= 0;
+        float2 s[4];
+        if (on)
+            scores32<CODE>(s, q, fmul2(qs, make_float2(k.ks, k.ks)), base + (2 * n) % kSlots * kSlot,
+                           lo - k.j * kBlk - ((threadIdx.x >> 5) & 1) * kHalfKeys);
+        reuse(2 * n + 3, 2 * blocks);
+        float2 a, b;
+        uint32_t pb[4];
+        if (on) {
+            soften(t, s, a, b);
+            // p as fp16, 2^-11 of it off at most: an eighth of what the output's own rounding to bf16 is, before the
+            // sum over keys evens it out (the sum of p itself is fp32)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pb[i] = transpose8(pack_half(s[i].x, s[i].y));
+        }
+        if (wait(2 * n + 1, where) && on)
+            values32<CODE>(t, pb, a, fmul2(b, make_float2(k.vs * kInvP, k.vs * kInvP)), base + (2 * n + 1) % kSlots * kSlot);
+        if (n + 2 < blocks && ((n + 2) & 31) == 0) mine = fetch((n + 2) >> 5);
+        reuse(2 * n + 4, 2 * blocks);
+        if (n + 2 < blocks) note(n + 2);
+        __syncwarp();
+    }
+    // After a wait that expired copies can be in flight: not past them.  `n`: the block the warp gave up at.
+    __device__ __forceinline__ void drain(int n, int blocks) {
+        if (!ok)
+            for (int c = max(0, 2 * n - 2); c < min(2 * blocks, 2 * n + 5); ++c)
+                mbar_wait_drain(&sm.full[c % kSlots], (c / kSlots) & 1);
+    }
+};
 
 }  // namespace zgcm

@@ -4,12 +4,13 @@
 // Bound by reading the codes: a block of one KV head is 16 KB and serves the few query heads of
 // its group.  What has to keep up with 43 bytes per SM and nanosecond is the conversion of the codes
 // and the two products; on CUDA cores the products alone are 8 multiply-adds per byte for 4
-// heads, more than an SM has.  So both run on the tensor cores as mma.sync m16n8k16 with
-// the heads as the 16 rows (a tcgen05 tile would have 4 of its 128 rows filled, and its
-// operands would have to go back to shared memory after their conversion):
-//   S = Q K^T: A = q of up to 8 heads (rows 0-7, zeros below), B = 8 keys x 16 dims.
-//   O = P V:   A = p in two 16-bit halves, rows 0-7 the rounded p, rows 8-15 what the rounding
-//              left (so the idle rows carry p to 22 bits), B = 16 keys x 8 dims.
+// heads, more than an SM has.  So both run on the tensor cores as mma.sync m16n8k16, the codes as the
+// 16-row operand and up to 8 heads as the 8 columns (in a tcgen05 tile the converted codes would have to go back
+// to shared memory, and its 128 rows would be heads, 4 of them real, or its smallest N twice these):
+//   S^T = K Q^T: 16 keys x 16 dims of codes by q of the heads;
+//   O^T = V^T P: 16 dims x 16 keys of codes by p, which is S^T's result transposed in registers (movmatrix).
+// (Heads as rows, zero-filled to 16, measured 1750 instructions a block against NNN here, p in two halves in
+// the idle rows included: the multiplier's four-register operand was half zeros.)
 // Codes become fp16 exactly and their scales multiply the fp32 sums, once per block: the scores by
 // ks, the block's O by vs where it joins the running O.  E4M3 pairs are converted by one instruction;
 // an INT8 code x as the byte x + 128 under the exponent of 1024, less 1152 (taking the 128 off the
@@ -18,13 +19,13 @@
 // power of two that brings the row's largest element to 2^14 (exact but for elements 2^-28 of it).
 //
 // Work: the blocks of every (sequence, KV head, 8 heads) — an item — and its tail are laid end to end
-// and cut into equal runs, one for each of 296 CTAs (two per SM), whatever the lengths; a CTA finds its
-// run from the positions on the device, so a captured graph follows them.  One warp fetches page
-// numbers and scales 32 blocks ahead and streams the codes by TMA (128-byte swizzle) into a ring of
-// 6 x 16 KB; each of four warps takes every 4th block with its own running maximum, sum and O.  At an
-// item's end the four are joined in a fixed order; an item that lies in one CTA is finished
-// there, pieces of a cut one go to the workspace and kv8_join_kernel finishes them (started early, by
+// and cut into equal runs, one for each of 592 CTAs (four per SM), whatever the lengths; a CTA finds its
+// run from the positions on the device, so a captured graph follows them.  Two of a CTA's four warps take a
+// block, 32 keys each, every warp with its own running maximum, sum and O and its own stream of copies
+// (kv8_attn.cuh).  At an item's end the four are joined in a fixed order; an item that lies in one CTA is finished
+// there, pieces of a cut one go to the workspace and kv8_join_kernel finishes them (launched early, by
 // programmatic dependent launch).  Results depend on positions and shapes alone.
+// Calls whose items have few blocks go to kv8_direct.cu.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -37,51 +38,45 @@ cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream);
 
 namespace {
 
-constexpr int DK_CTAS = 296;               // 148 SMs x 2
-constexpr int DK_WARPS = 4;                // warps that compute; one more loads
-constexpr int DK_THREADS = (DK_WARPS + 1) * 32;
-constexpr int DK_STAGES = 6;
+constexpr int DK_CTAS = 592;               // 148 SMs x 4
+constexpr int DK_THREADS = 128;
 constexpr int DK_POS = 64;                 // positions of the run's sequences kept in shared memory
 constexpr int DK_REC = kD + 4;             // floats of a record's head: m, l, 2 pad, O
-constexpr int DK_WAIT_LOAD = 0x810, DK_WAIT_RING = 0x811;
-
-struct DecodeSmem {
-    alignas(1024) unsigned char k[DK_STAGES][kBlkBytes];
-    alignas(1024) unsigned char v[DK_STAGES][kBlkBytes];
-    float acc[2][DK_HEADS][kD];
-    float ml[DK_WARPS][DK_HEADS][2];
-    Meta meta[DK_STAGES];
-    uint64_t full[DK_STAGES], empty[DK_STAGES];
-    int pos[DK_POS];
-    long long lo, hi;
-    int b0, rest0, off0;
-    int abort;
-};
-static_assert(2 * (sizeof(DecodeSmem) + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
-
-__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// ------------------------------------------------------------------ the walk over the units
+constexpr int DK_WAIT = 0x810;
 
 struct Walk {
     int b, rest, off;   // sequence, item of it, unit of the item
 };
 
+struct DecodeSmem {
+    alignas(1024) unsigned char ring[4][kSlots * kSlot];
+    float acc[DK_HEADS][kD];
+    float ml[4][DK_HEADS][2];
+    WarpSmem warp[4];
+    int pos[DK_POS];
+    long long sum[4];
+    Walk start, end;
+    int abort;
+};
+static_assert(4 * (sizeof(DecodeSmem) + 1024 + 1024) <= 228 * 1024, "four CTAs per SM");
+
+// ------------------------------------------------------------------ the walk over the units
+
 struct Run {
     const DecodeKv8Params& p;
     const DecodeSmem& sm;
     __device__ __forceinline__ int pos(int b) const {
-        const int i = b - sm.b0;
+        const int i = b - sm.start.b;
         return i < DK_POS ? sm.pos[i] : p.pos[b];
     }
-    // n units on; stays at the end when it runs past it
-    __device__ __forceinline__ void step(Walk& w, int n) const {
+    // n units on (8-bit ones alone if `codes`); stays at the end when it runs past it
+    template <bool codes> __device__ __forceinline__ void step(Walk& w, int n) const {
         w.off += n;
         const int items = p.c.Hkv * p.HT;
         while (w.b < p.c.B) {
-            const int u = span_of(p, pos(w.b)).units;
+            const int u = span_of(p, pos(w.b)).units - (codes ? 1 : 0);
             if (w.off < u) return;
-            const int skip = min(w.off / u, items - w.rest);
+            const int skip = u > 0 ? min(w.off / u, items - w.rest) : items - w.rest;
             w.off -= skip * u;
             w.rest += skip;
             if (w.rest < items) return;
@@ -90,15 +85,6 @@ struct Run {
         }
     }
 };
-
-// units before sequence b, and in all, by one warp: *total, and the sequence that holds unit x
-__device__ __forceinline__ long long count_units(const DecodeKv8Params& p, int upto) {
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < upto; b += 32) n += span_of(p, p.pos[b]).units;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * (p.c.Hkv * p.HT);
-}
 
 // Runs: as many as there are CTAs, or units when those are fewer (no run between two others is empty: an
 // item's records are those of all CTAs from its first to its last).
@@ -112,91 +98,107 @@ __device__ __forceinline__ int run_of(long long total, long long x) {
     return (int)(((x + 1) * run_count(total) - 1) / total);
 }
 
-// ------------------------------------------------------------------ loading warp
-
-__device__ __forceinline__ void load_run(const DecodeKv8Params& p, DecodeSmem& sm, const Run& run, long long lo, long long hi) {
-    const int lane = threadIdx.x & 31;
-    Walk at{sm.b0, sm.rest0, sm.off0};
-    int slot = 0;
-    bool ok = true;
-    for (long long x = lo; x < hi && ok; x += 32) {
-        Walk w = at;
-        run.step(w, lane);
-        Tile tile{-1, -1, 0.f, 0.f};
-        bool is8 = false;
-        int kvh = 0;
-        if (x + lane < hi) {
-            const Span s = span_of(p, run.pos(w.b));
-            is8 = w.off < s.units - 1;
-            kvh = w.rest / p.HT;
-            if (is8) tile = tile_of(p, s, w.b, kvh, w.off);
-        }
-        const uint32_t all = __ballot_sync(0xffffffffu, is8);
-        for (uint32_t left = all; left; left &= left - 1, ++slot) {
-            const int st = slot % DK_STAGES;
-            if (lane == __ffs(left) - 1) {
-                if (slot >= DK_STAGES && !mbar_wait(&sm.empty[st], (slot / DK_STAGES - 1) & 1, &sm.abort, DK_WAIT_RING))
-                    ok = false;
-                if (ok) {
-                    sm.meta[st] = Meta{tile.ks, tile.vs, tile.j, 0};
-                    if (tile.page >= 0) {
-                        const int row = (tile.page * p.c.Hkv + kvh) * kBlk;
-                        mbar_expect_tx(&sm.full[st], 2 * kBlkBytes);
-                        tma_load_2d(sm.k[st], &p.tm_k, &sm.full[st], 0, row);
-                        tma_load_2d(sm.v[st], &p.tm_v, &sm.full[st], 0, row);
-                    } else {
-                        mbar_arrive(&sm.full[st]);
-                    }
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-        }
-        run.step(at, 32);
-    }
-    // copies in flight (after a wait that expired there can be some): not before they have landed
-    if (lane == 0)
-        for (int s = max(0, slot - DK_STAGES); s < slot; ++s) mbar_wait_drain(&sm.full[s % DK_STAGES], (s / DK_STAGES) & 1);
+// Sums over a block of 128 threads; `sum` [4] in shared memory.
+__device__ __forceinline__ long long cta_sum(long long x, long long* sum) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return sum[0] + sum[1] + sum[2] + sum[3];
 }
 
-// ------------------------------------------------------------------ computing warps
+// The run of this CTA, into sm.start and sm.end; returns its number of units.
+__device__ __forceinline__ int find_run(const DecodeKv8Params& p, DecodeSmem& sm) {
+    const int tid = threadIdx.x, lane = tid & 31, items = p.c.Hkv * p.HT;
+    const int first = tid < p.c.B ? span_of(p, p.pos[tid]).units : 0;
+    long long n = first;
+    for (int b = tid + DK_THREADS; b < p.c.B; b += DK_THREADS) n += span_of(p, p.pos[b]).units;
+    const long long total = cta_sum(n, sm.sum) * items;
+    const long long lo = run_start(total, blockIdx.x), hi = run_start(total, blockIdx.x + 1);
+    if (tid == 0) sm.start = sm.end = Walk{p.c.B, 0, 0};
+    long long before = 0;   // units of the sequences before these 128
+    for (int b0 = 0; b0 < p.c.B; b0 += DK_THREADS) {
+        const int b = b0 + tid;
+        const int u = b0 == 0 ? first : b < p.c.B ? span_of(p, p.pos[b]).units : 0;
+        long long s = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        __syncthreads();
+        if (lane == 31) sm.sum[tid >> 5] = s;
+        __syncthreads();
+        long long at = before + s - u;
+        for (int w = 0; w < (tid >> 5); ++w) at += sm.sum[w];
+        before += sm.sum[0] + sm.sum[1] + sm.sum[2] + sm.sum[3];
+        // this thread's sequence has units [at, at + u) * items
+        if (u > 0) {
+            const long long x = at * items, y = x + (long long)u * items;
+            if (lo >= x && lo < y) sm.start = Walk{b, (int)((lo - x) / u), (int)((lo - x) % u)};
+            if (hi >= x && hi < y) sm.end = Walk{b, (int)((hi - x) / u), (int)((hi - x) % u)};
+        }
+        if (before * items > hi) break;
+    }
+    __syncthreads();
+    for (int i = tid; i < DK_POS; i += DK_THREADS)
+        if (sm.start.b + i < p.c.B) sm.pos[i] = p.pos[sm.start.b + i];
+    __syncthreads();
+    return (int)(hi - lo);
+}
+
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <typename TK, int CODE>
-__device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem& sm, const Run& run, long long lo,
-                                            long long hi) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    Walk w{sm.b0, sm.rest0, sm.off0};
-    int slot = 0;   // 8-bit units of the run so far: the ring's slots, slot s for warp s % 4
-    for (long long x = lo; x < hi;) {
+__global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_constant__ DecodeKv8Params p) {
+    extern __shared__ unsigned char raw[];
+    DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may take its place early
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(&sm.warp[warp].full[i], 1);
+        if (warp == 0) sm.abort = 0;
+        fence_barrier_init();
+    }
+    const int units = find_run(p, sm);
+    const Run run{p, sm};
+    const int items = p.c.Hkv * p.HT, team = warp >> 1;
+    // the 8-bit units of the run: all but the tails, one at the end of each item that ends in it
+    const int n_codes = units - ((sm.end.b - sm.start.b) * items + sm.end.rest - sm.start.rest);
+    const int blocks = (n_codes - team + 1) / 2;       // this pair's: every second one
+    Walk ahead = sm.start;                             // the 8-bit unit `taken` of the run
+    run.step<true>(ahead, 0);
+    int taken = 0;
+    auto fetch = [&](int batch) {                      // lane i: the pair's block 32 batch + i; batches in order
+        run.step<true>(ahead, 64 * batch - taken);
+        taken = 64 * batch;
+        Walk w = ahead;
+        run.step<true>(w, team + 2 * lane);
+        if (32 * batch + lane >= blocks) return Block{-1, -1, 0.f, 0.f};
+        return block_of(p, span_of(p, run.pos(w.b)), w.b, w.rest / p.HT, w.off);
+    };
+    Stream stream(p, sm.warp[warp], sm.ring[warp], &sm.abort);
+    stream.mine = fetch(0);
+    stream.start(blocks);
+
+    Walk w = sm.start;
+    int slot = 0, gave_up = 0;   // 8-bit units of the run so far
+    for (int left = units; left > 0;) {
         const Span s = span_of(p, run.pos(w.b));
-        const int n = (int)min((long long)(s.units - w.off), hi - x);          // units of the item here
+        const int n = min(s.units - w.off, left);                              // units of the item here
         const int n8 = max(0, min(w.off + n, s.units - 1) - w.off);
         const bool has_tail = w.off + n == s.units;
         const int kvh = w.rest / p.HT, ht = w.rest % p.HT;
         const int nh = min(DK_HEADS, p.G - ht * DK_HEADS);
         const size_t head = (size_t)w.b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS + r;   // this lane's head (r < nh)
         const bool one = w.off == 0 && has_tail;                               // the whole item
-        State t;
-        t.m = -INFINITY;
-        t.l = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t.e[i] = t.o[i] = make_float2(0.f, 0.f);
         if (s.idle || s.bad) {
             if (warp == 0 && r < nh) no_answer(p, head, s.idle);
         } else {
+            State t;
             uint32_t qt[8][2], q16[8][2];   // as they are, for the tail; as fp16, for codes
             load_q<TK>(p, head, r < nh, qt);
-            const float qs = q_as_half<TK>(p, qt, q16);
-            for (int i = ((warp >> 1) - slot) & 1; i < n8; i += 2) {
-                const int sl = slot + i, st = sl % DK_STAGES;
-                if (mbar_wait(&sm.full[st], (sl / DK_STAGES) & 1, &sm.abort, DK_WAIT_LOAD)) {
-                    const Meta meta = sm.meta[st];
-                    if (meta.j >= 0)
-                        block8<CODE>(t, q16, qs, smem_u32(sm.k[st]), smem_u32(sm.v[st]), meta, s.lo, (warp & 1) * 32);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.empty[st]);
-            }
             if (has_tail) {
                 const int last = run.pos(w.b) - s.own * kBlk, first = s.lo - s.own * kBlk;
                 if (warp * 16 <= last && warp * 16 + 15 >= first) {
@@ -205,129 +207,61 @@ __device__ __forceinline__ void compute_run(const DecodeKv8Params& p, DecodeSmem
                                first, last);
                 }
             }
-            // the four warps' parts into warp 0's, always in the same order
-            t.l += __shfl_xor_sync(0xffffffffu, t.l, 1);
-            t.l += __shfl_xor_sync(0xffffffffu, t.l, 2);
-            if (c == 0) {
-                sm.ml[warp][r][0] = t.m;
-                sm.ml[warp][r][1] = t.l;
+            const float2 qs = q_as_half<TK>(p, qt, q16);
+            for (int i = (team - slot) & 1; i < n8; i += 2) {
+                const int k = (slot + i) >> 1;
+                if (stream.ok) gave_up = k;
+                stream.take<CODE>(t, q16, qs, s.lo, k, blocks, DK_WAIT, fetch);
             }
+            // the four warps' parts, always added in the same order
+            put_ml(t, sm.ml[warp]);
             warps_sync();
-            float m = -INFINITY, l = 0.f, f = 0.f;
+            float m, l;
+            const float fx = join_ml(sm.ml, 2 * c, warp, m, l), fy = join_ml(sm.ml, 2 * c + 1, warp, m, l);
 #pragma unroll
-            for (int i = 0; i < DK_WARPS; ++i) m = fmaxf(m, sm.ml[i][r][0]);
+            for (int from = 3; from >= 0; --from) {
+                if (warp == from) {
 #pragma unroll
-            for (int i = 0; i < DK_WARPS; ++i) {
-                // a part without keys counts nothing; one whose scores were all NaN has a NaN sum
-                const float fi = sm.ml[i][r][1] == 0.f ? 0.f : fast_exp2(sm.ml[i][r][0] - m);
-                l = fmaf(sm.ml[i][r][1], fi, l);
-                if (i == warp) f = fi;
+                    for (int i = 0; i < 8; ++i) {
+                        float2* x = reinterpret_cast<float2*>(&sm.acc[2 * c][16 * i + 2 * r]);
+                        float2* y = reinterpret_cast<float2*>(&sm.acc[2 * c + 1][16 * i + 2 * r]);
+                        float2 u = make_float2(t.o[i][0].x * fx, t.o[i][1].x * fx);
+                        float2 v = make_float2(t.o[i][0].y * fy, t.o[i][1].y * fy);
+                        if (from < 3) {
+                            u = fadd2(u, *x);
+                            v = fadd2(v, *y);
+                        }
+                        *x = u;
+                        *y = v;
+                    }
+                }
+                warps_sync();
             }
-            const float2 ff = make_float2(f, f);
+            // 256 places of a head and 4 dims
+            const size_t item = ((size_t)w.b * p.c.Hkv + kvh) * p.HT + ht;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                t.e[i] = fmul2(t.e[i], ff);
-                t.o[i] = fmul2(t.o[i], ff);
-            }
-            if (warp >= 2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<float4*>(&sm.acc[warp - 2][r][16 * i + 4 * c]) =
-                        make_float4(t.e[i].x, t.o[i].x, t.e[i].y, t.o[i].y);
-            }
-            warps_sync();
-            if (warp < 2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float4* a = reinterpret_cast<float4*>(&sm.acc[warp][r][16 * i + 4 * c]);
-                    const float4 y = *a;
-                    t.e[i] = fadd2(t.e[i], make_float2(y.x, y.z));
-                    t.o[i] = fadd2(t.o[i], make_float2(y.y, y.w));
-                    if (warp == 1) *a = make_float4(t.e[i].x, t.o[i].x, t.e[i].y, t.o[i].y);
+            for (int i = 0; i < 2; ++i) {
+                const int h = (tid + DK_THREADS * i) >> 5, d = 4 * (tid & 31);
+                if (h < nh) {
+                    join_ml(sm.ml, h, 0, m, l);
+                    const float4 y = *reinterpret_cast<const float4*>(&sm.acc[h][d]);
+                    const float o[4] = {y.x, y.y, y.z, y.w};
+                    if (one) {
+                        finish4(p, head - r + h, d, m, l, o);
+                    } else {
+                        float* rec = p.part + ((item + blockIdx.x) * p.rows + h) * DK_REC;
+                        if (d == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+                        *reinterpret_cast<float4*>(rec + 4 + d) = y;
+                    }
                 }
             }
-            warps_sync();
-            if (warp == 0 && r < nh) {
-                const size_t item = ((size_t)w.b * p.c.Hkv + kvh) * p.HT + ht;
-                float* rec = p.part + ((item + blockIdx.x) * p.rows + r) * DK_REC;
-                if (!one && c == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 y = *reinterpret_cast<const float4*>(&sm.acc[1][r][16 * i + 4 * c]);
-                    const float o[4] = {t.e[i].x + y.x, t.o[i].x + y.y, t.e[i].y + y.z, t.o[i].y + y.w};
-                    if (one)
-                        finish4(p, head, 16 * i + 4 * c, m, l, o);
-                    else
-                        *reinterpret_cast<float4*>(rec + 4 + 16 * i + 4 * c) = make_float4(o[0], o[1], o[2], o[3]);
-                }
-            }
+            warps_sync();   // the next item may write what these have read
         }
         slot += n8;
-        x += n;
-        run.step(w, n);
+        left -= n;
+        run.step<false>(w, n);
     }
-}
-
-template <typename TK, int CODE>
-__global__ void __launch_bounds__(DK_THREADS, 2) kv8_decode_kernel(const __grid_constant__ DecodeKv8Params p) {
-    extern __shared__ unsigned char raw[];
-    DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may take its place early
-    if (warp == DK_WARPS) {
-        if (lane == 0) {
-            for (int i = 0; i < DK_STAGES; ++i) {
-                mbar_init(&sm.full[i], 1);
-                mbar_init(&sm.empty[i], 2);
-            }
-            sm.abort = 0;
-            fence_barrier_init();
-            prefetch_tmap(&p.tm_k);
-            prefetch_tmap(&p.tm_v);
-        }
-    } else if (warp == 0) {
-        const int items = p.c.Hkv * p.HT;
-        const long long total = count_units(p, p.c.B);
-        const long long lo = run_start(total, blockIdx.x), hi = run_start(total, blockIdx.x + 1);
-        // the sequence that holds unit lo, 32 sequences at a time
-        long long before = 0;
-        int b0 = 0;
-        for (int b = 0; b < p.c.B; b += 32) {
-            const long long u = b + lane < p.c.B ? (long long)span_of(p, p.pos[b + lane]).units * items : 0;
-            long long s = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += y;
-            }
-            const uint32_t in = __ballot_sync(0xffffffffu, before + s > lo);
-            if (in) {
-                const int f = __ffs(in) - 1;
-                b0 = b + f;
-                before += __shfl_sync(0xffffffffu, s - u, f);
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, s, 31);
-        }
-        if (lane == 0) {
-            const int u = span_of(p, p.pos[b0]).units;
-            const long long in = lo - before;
-            sm.lo = lo;
-            sm.hi = hi;
-            sm.b0 = b0;
-            sm.rest0 = (int)(in / u);
-            sm.off0 = (int)(in % u);
-        }
-        for (int i = lane; i < DK_POS; i += 32)
-            if (b0 + i < p.c.B) sm.pos[i] = p.pos[b0 + i];
-    }
-    __syncthreads();
-    const Run run{p, sm};
-    const long long lo = sm.lo, hi = sm.hi;
-    if (warp == DK_WARPS)
-        load_run(p, sm, run, lo, hi);
-    else
-        compute_run<TK, CODE>(p, sm, run, lo, hi);
+    stream.drain(gave_up, blocks);
     __syncthreads();
     if (tid == 0 && sm.abort) *p.err = sm.abort;
 }
@@ -339,8 +273,15 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ D
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int item = blockIdx.x / p.rows, row = blockIdx.x % p.rows;
     const int items = p.c.Hkv * p.HT, b = item / items, rest = item % items, kvh = rest / p.HT, ht = rest % p.HT;
+    __shared__ long long sum[4];
     const int units = span_of(p, p.pos[b]).units;
-    const long long total = count_units(p, p.c.B), start = count_units(p, b) + (long long)rest * units;
+    long long all = 0, before = 0;
+    for (int i = threadIdx.x; i < p.c.B; i += 128) {
+        const int u = span_of(p, p.pos[i]).units;
+        all += u;
+        if (i < b) before += u;
+    }
+    const long long total = cta_sum(all, sum) * items, start = cta_sum(before, sum) * items + (long long)rest * units;
     const int c0 = run_of(total, start), c1 = run_of(total, start + units - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");   // every block: the grid must not end before the records' writer
     if (c0 == c1 || ht * DK_HEADS + row >= p.G) return;
@@ -394,7 +335,7 @@ bool make_map(CUtensorMap* map, const void* codes, const Kv8& c) {
     if (!enc) return false;
     cuuint64_t dims[2] = {kD, (cuuint64_t)c.P * c.Hkv * kBlk};
     cuuint64_t strides[1] = {kD};
-    cuuint32_t box[2] = {kD, kBlk}, estr[2] = {1, 1};
+    cuuint32_t box[2] = {kD, kHalfKeys}, estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

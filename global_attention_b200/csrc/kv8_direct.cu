@@ -6,8 +6,7 @@
 // cluster of 1 to 8 CTAs takes an item whose units are split evenly among them; nothing but its own position
 // decides a CTA's work, the rows of q and of the tail load while page numbers do, the CTAs' parts meet in
 // shared memory across the cluster (each finishes a share of the dims), and there is no second kernel.  Four CTAs of
-// four warps fit on an SM: their latencies overlap.  Two warps share a block, 32 keys each; the
-// first of them also fetches the pair's page numbers, 32 blocks ahead, and keeps the pair's half of the ring full.
+// four warps fit on an SM: their latencies overlap.
 #include <cooperative_groups.h>
 
 #include "kv8_attn.cuh"
@@ -18,12 +17,12 @@ namespace zgcm {
 namespace {
 
 constexpr int DD_THREADS = 128;
-constexpr int DD_MAX_STAGES = 4;
-constexpr int DD_WAIT_LOAD = 0x820, DD_WAIT_RING = 0x821;
+constexpr int DD_WAIT = 0x820;
+constexpr size_t DD_RING = 4 * kSlots * kSlot;
+static_assert(DD_RING >= 5 * DK_HEADS * kD * sizeof(float), "the warps' parts and their sum take the ring's place");
 
 struct DirectSmem {
-    uint64_t full[DD_MAX_STAGES], empty[DD_MAX_STAGES];
-    Meta meta[DD_MAX_STAGES];
+    WarpSmem warp[4];
     float ml[4][DK_HEADS][2];
     float cta_ml[DK_HEADS][2];
     int abort;
@@ -43,12 +42,9 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     const int pos = p.pos[b];
     uint32_t qt[8][2];
     load_q<TK>(p, head0 + r, r < nh, qt);
-    if (tid == 0) {
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&sm.full[i], 2);    // the codes' bytes, and the scales
-            mbar_init(&sm.empty[i], 2);   // the pair
-        }
-        sm.abort = 0;
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(&sm.warp[warp].full[i], 1);
+        if (warp == 0) sm.abort = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -57,47 +53,18 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         if (rank == 0 && warp == 0 && r < nh) no_answer(p, head0 + r, s.idle);
         return;
     }
-    // this CTA's blocks, and of them this pair's: every second one
+    // this CTA's blocks, and of them this warp's pair's: every second one
     const int n8 = s.units - 1, u0 = (int)((long long)n8 * rank / p.split), u1 = (int)((long long)n8 * (rank + 1) / p.split);
-    const int team = warp >> 1, per = p.stages / 2, nt = (u1 - u0 - team + 1) / 2;
-    unsigned char* base = ring + team * per * 2 * kBlkBytes;
-    uint64_t *full = sm.full + team * per, *empty = sm.empty + team * per;
-    Meta* meta = sm.meta + team * per;
-    const bool loads = (warp & 1) == 0;
-    Tile tile{-1, -1, 0.f, 0.f};
+    const int team = warp >> 1, nt = (u1 - u0 - team + 1) / 2;
+    Stream stream(p, sm.warp[warp], ring + warp * kSlots * kSlot, &sm.abort);
     auto fetch = [&](int batch) {   // lane i: the pair's block 32 batch + i
         const int k = 32 * batch + lane;
-        tile = Tile{-1, -1, 0.f, 0.f};
-        if (k < nt) tile = tile_of(p, s, b, kvh, u0 + team + 2 * k);
+        return k < nt ? block_of(p, s, b, kvh, u0 + team + 2 * k) : Block{-1, -1, 0.f, 0.f};
     };
-    auto codes = [&](int k) {       // by the lane that holds block k
-        const int st = k % per;
-        if (tile.page >= 0) {
-            const int row = (tile.page * p.c.Hkv + kvh) * kBlk;
-            mbar_expect_tx(&full[st], 2 * kBlkBytes);
-            tma_load_2d(base + st * 2 * kBlkBytes, &p.tm_k, &full[st], 0, row);
-            tma_load_2d(base + st * 2 * kBlkBytes + kBlkBytes, &p.tm_v, &full[st], 0, row);
-        } else {
-            mbar_arrive(&full[st]);
-        }
-    };
-    auto scales = [&](int k) {
-        meta[k % per] = Meta{tile.ks, tile.vs, tile.j, 0};
-        mbar_arrive(&full[k % per]);
-    };
-    if (loads) {
-        fetch(0);
-        // all codes first: the scales are still on their way
-        if (lane < min(per, nt)) codes(lane);
-        if (lane < min(per, nt)) scales(lane);
-        __syncwarp();
-    }
+    stream.mine = fetch(0);
+    stream.start(nt);
 
     State t;
-    t.m = -INFINITY;
-    t.l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t.e[i] = t.o[i] = make_float2(0.f, 0.f);
     if (rank == 0) {
         const int last = pos - s.own * kBlk, first = s.lo - s.own * kBlk;
         if (warp * 16 <= last && warp * 16 + 15 >= first) {
@@ -106,69 +73,31 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         }
     }
     uint32_t q16[8][2];
-    const float qs = q_as_half<TK>(p, qt, q16);
-    bool ok = true;
-    int issued = min(per, nt);
+    const float2 qs = q_as_half<TK>(p, qt, q16);
+    int gave_up = 0;
     for (int k = 0; k < nt; ++k) {
-        const int st = k % per, phase = (k / per) & 1;
-        if (ok && mbar_wait(&full[st], phase, &sm.abort, DD_WAIT_LOAD)) {
-            const Meta m = meta[st];
-            if (m.j >= 0)
-                block8<CODE>(t, q16, qs, smem_u32(base + st * 2 * kBlkBytes), smem_u32(base + st * 2 * kBlkBytes + kBlkBytes), m,
-                             s.lo, (warp & 1) * 32);
-        } else {
-            ok = false;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-        const int next = k + per;
-        if (loads && next < nt) {
-            if (next % 32 == 0) fetch(next / 32);
-            if (ok && lane == next % 32) {
-                if (mbar_wait(&empty[st], phase, &sm.abort, DD_WAIT_RING)) {
-                    codes(next);
-                    scales(next);
-                } else {
-                    ok = false;
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) ++issued;
-        }
+        if (stream.ok) gave_up = k;
+        stream.take<CODE>(t, q16, qs, s.lo, k, nt, DD_WAIT, fetch);
     }
-    // a wait that expired leaves copies in flight: not past them
-    if (loads && !ok)
-        for (int k = max(0, issued - per); k < issued; ++k) mbar_wait_drain(&full[k % per], (k / per) & 1);
+    stream.drain(gave_up, nt);
 
     // the warps' parts, in a fixed order; the ring is free once all have come here
     float(*acc)[DK_HEADS][kD] = reinterpret_cast<float(*)[DK_HEADS][kD]>(ring);                      // [warp]
     float(*sum)[kD] = reinterpret_cast<float(*)[kD]>(ring + 4 * DK_HEADS * kD * sizeof(float));      // the CTA's
-    t.l += __shfl_xor_sync(0xffffffffu, t.l, 1);
-    t.l += __shfl_xor_sync(0xffffffffu, t.l, 2);
-    if (c == 0) {
-        sm.ml[warp][r][0] = t.m;
-        sm.ml[warp][r][1] = t.l;
-    }
+    put_ml(t, sm.ml[warp]);
     __syncthreads();
-    float m = -INFINITY, l = 0.f, f = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, sm.ml[i][r][0]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // a part without keys counts nothing; one whose scores were all NaN has a NaN sum
-        const float fi = sm.ml[i][r][1] == 0.f ? 0.f : fast_exp2(sm.ml[i][r][0] - m);
-        l = fmaf(sm.ml[i][r][1], fi, l);
-        if (i == warp) f = fi;
-    }
-    const float2 f2 = make_float2(f, f);
+    float m, l;
+    const float fx = join_ml(sm.ml, 2 * c, warp, m, l), fy = join_ml(sm.ml, 2 * c + 1, warp, m, l);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 x = fmul2(t.e[i], f2), y = fmul2(t.o[i], f2);
-        *reinterpret_cast<float4*>(&acc[warp][r][16 * i + 4 * c]) = make_float4(x.x, y.x, x.y, y.y);
+        const int d = 16 * i + 2 * r;
+        *reinterpret_cast<float2*>(&acc[warp][2 * c][d]) = make_float2(t.o[i][0].x * fx, t.o[i][1].x * fx);
+        *reinterpret_cast<float2*>(&acc[warp][2 * c + 1][d]) = make_float2(t.o[i][0].y * fy, t.o[i][1].y * fy);
     }
-    if (warp == 0 && c == 0) {
-        sm.cta_ml[r][0] = m;
-        sm.cta_ml[r][1] = l;
+    if (tid < DK_HEADS) {
+        join_ml(sm.ml, tid, 0, m, l);
+        sm.cta_ml[tid][0] = m;
+        sm.cta_ml[tid][1] = l;
     }
     __syncthreads();
     // 256 places of a head and 4 dims
@@ -217,9 +146,8 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
 }
 
 template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
-    const size_t smem = (size_t)p.stages * 2 * kBlkBytes + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DD_MAX_STAGES * 2 * kBlkBytes + 1024);
+    const size_t smem = DD_RING + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * p.HT * p.split));
@@ -242,7 +170,6 @@ bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
     while (p.split < 8 && items * p.split * 2 <= 592 && units > 2 * p.split) p.split *= 2;
-    p.stages = items * p.split <= 296 && units > 4 * p.split ? 4 : 2;
     return units <= 64 * p.split && items * p.split <= 0x7fffffffLL;
 }
 

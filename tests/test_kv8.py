@@ -3,15 +3,14 @@ checks on the CPU, results on the B200 against the oracle of the definition (ora
 
 Tolerances, from the arithmetic.  Codes, scales and tails: none (the definition's fp32 steps
 are the kernel's).  Block means: fp32 sums of 64 (20 additions deep, 2^-24 each) and one
-rounding to the keys' type.  Attention, u = 2^-24: a score is an fp32 sum of 128 products, 128u of the
-sum of their magnitudes at most, times fp32 scales (4u), so each probability is off by a
-factor within e = 2^-16 sum |q k| scale at most (its own error and the normaliser's), exp2 2^-22
-and its 16-bit halves 2^-20; a score's rounding in base 2 adds 2^-24 |s|, covered by the same
-bound; sums of up to 2^16 keys in tiles and partial records 2^-17.  The output is then rounded once
-to bf16 (2^-8 of the value): 2^-8 |ref| + (2 e + 2^-15) sum p |v|.  lse: e + 2^-17 + 2^-22 |lse|.
-A probability enters the second product as two fp16 halves of p 2^14 relative to its block's largest: off by half
-their smallest step, 2^-25 / 2^14 = 2^-39 of that, for each of 64 keys: 2^-33 of the block's p times its
-largest |v| (2^-15 sum p |v| covers the rest, 2^-22 relative).
+rounding to the keys' type.  Attention, u = 2^-24:
+a score is an fp32 sum of 128 products, 128u of the sum of their magnitudes at most, times fp32 scales (4u), so each
+probability is off by a factor within e = 2^-16 sum |q k| scale at most (its own error and the normaliser's), exp2 by
+2^-22; a score's rounding in base 2 adds 2^-24 |s|, covered by the same bound; sums of up to 2^16 keys in tiles and partial
+records 2^-17.  A block's p enters the second product as fp16, 2^-11 of it off, or, below fp16's normal numbers, half their
+step: p 2^14 is relative to its block's largest, so 2^-25 / 2^14 = 2^-39 of that for each of 64 keys, 2^-33 of the block's p
+times its largest |v|.  The output is rounded once to bf16 (2^-8 of the value).  Together
+2^-8 |ref| + (2 e + 2^-11 + 2^-15) sum p |v| + 2^-33 sum of blocks' p max |v|.  lse: e + 2^-17 + 2^-22 |lse|.
 Selected blocks: equal.
 """
 import ctypes
@@ -273,7 +272,7 @@ def _close(name, out, lse, ref, ref_lse, mag, top, q, k, scale):
     qk = np.array([(np.abs(q[h].double().numpy()) * km[h // G]).sum() for h in range(len(q))]) * scale * 1.0625
     e = (2.0 ** -16 * qk)[:, None]
     got = out.double().cpu().numpy()
-    err = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) * 1.001 + (2 * e + 2.0 ** -15) * mag + 2.0 ** -33 * top[:, None] + 1e-37)
+    err = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) * 1.001 + (2 * e + 2.0 ** -11 + 2.0 ** -15) * mag + 2.0 ** -33 * top[:, None] + 1e-37)
     assert np.isfinite(got).all() and (err <= 0).all(), (name, float(err.max()))
     err = np.abs(lse.double().cpu().numpy() - ref_lse) - (e[:, 0] + 2.0 ** -17 + 2.0 ** -22 * np.abs(ref_lse))
     assert (err <= 0).all(), (name, "lse", float(err.max()))
