@@ -250,25 +250,37 @@ __device__ __forceinline__ void values32(State& t, const uint32_t (&pb)[4], floa
 
 // 16 keys of the tail, k0 .. k0 + 15 of its block, valid where first <= key <= last; 16-bit products of the
 // types as they are (values in bf16 span more than fp16 does, so p goes in as two bf16, 16 bits of it)
-template <typename TK>
-__device__ __forceinline__ void tail16(State& t, const uint32_t (&q)[8][2], float scale, const TK* k, const bf16* v, int k0,
-                                       int first, int last) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+template <typename TK> struct Tail {
     uint2 kw[2][8];
     uint32_t vw[8][4];
+    __device__ __forceinline__ void load(const DecodeKv8Params& p, size_t seq_head, int k0) {
+        const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+        const TK* k = reinterpret_cast<const TK*>(p.c.ktail) + seq_head * kBlkBytes + 4 * c;
+        const bf16* v = p.c.vtail + seq_head * kBlkBytes + 2 * r;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const TK* row = k + (k0 + 8 * n + r) * kD + 4 * c;
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) kw[n][i] = *reinterpret_cast<const uint2*>(row + 16 * i);
+            for (int i = 0; i < 8; ++i) kw[n][i] = *reinterpret_cast<const uint2*>(k + (k0 + 8 * n + r) * kD + 16 * i);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                vw[i][x] = *reinterpret_cast<const uint32_t*>(v + (k0 + 2 * c + (x & 1) + 8 * (x >> 1)) * kD + 16 * i);
     }
+    __device__ __forceinline__ void take(State& t, const uint32_t (&q)[8][2], float scale, int k0, int first, int last);
+};
+
+template <typename TK>
+__device__ __forceinline__ void Tail<TK>::take(State& t, const uint32_t (&q)[8][2], float scale, int k0, int first, int last) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int key = k0 + 2 * c + (x & 1) + 8 * (x >> 1);
-        const bool on = key >= first && key <= last;
         // a masked row may hold anything: it must not reach the product
+        if (key < first || key > last) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vw[i][x] = on ? *reinterpret_cast<const uint32_t*>(v + key * kD + 16 * i + 2 * r) : 0u;
+            for (int i = 0; i < 8; ++i) vw[i][x] = 0u;
+        }
     }
     float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -330,13 +342,17 @@ __device__ __forceinline__ float join_ml(const float (*ml)[DK_HEADS][2], int h, 
     return f;
 }
 
+__device__ __forceinline__ uint2 load_gate(const DecodeKv8Params& p, size_t head, int d) {
+    return p.g ? *reinterpret_cast<const uint2*>(p.g + head * kD + d) : make_uint2(0u, 0u);
+}
+
 // out and lse of four dims of one head from its maximum, sum and O
-__device__ __forceinline__ void finish4(const DecodeKv8Params& p, size_t head, int d, float m, float l, const float (&o)[4]) {
+__device__ __forceinline__ void finish4(const DecodeKv8Params& p, size_t head, int d, float m, float l, const float (&o)[4],
+                                        uint2 gate) {
     const float inv = 1.f / (l * kInvP);
     float x[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
     if (p.g) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p.g + head * kD + d);
-        const float2 a = unpack_bf16(w.x), b = unpack_bf16(w.y);
+        const float2 a = unpack_bf16(gate.x), b = unpack_bf16(gate.y);
         x[0] *= sigmoidf_(a.x);
         x[1] *= sigmoidf_(a.y);
         x[2] *= sigmoidf_(b.x);
@@ -419,13 +435,17 @@ struct Block {       // as the lane that holds it knows it
 // Block number `i` of an item's 8-bit units
 __device__ __forceinline__ Block block_of(const DecodeKv8Params& p, const Span& s, int b, int kvh, int i) {
     Block t{s.jlo + i, -1, 0.f, 0.f};
+    int page = -1;
     if (p.blocks) {
         const int* list = p.blocks + ((size_t)b * p.c.Hkv + kvh) * p.n_list + i;
+        const int before = i > 0 ? list[-1] : -1;
         t.j = *list;
-        if (t.j < s.jlo || t.j >= s.own || (i > 0 && t.j <= list[-1])) t.j = -1;
+        if (t.j >= 0) page = kv8_page(p.c, b, t.j);   // before s, which waits for the position, is asked
+        if (t.j < s.jlo || t.j >= s.own || t.j <= before) t.j = -1;
+    } else {
+        page = kv8_page(p.c, b, t.j);
     }
     if (t.j >= 0) {
-        const int page = kv8_page(p.c, b, t.j);
         t.ks = t.vs = NAN;          // a bad page reads as NaN
         if (page >= 0) {
             const int at = page * p.c.Hkv + kvh;

@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_
             if (has_tail) {
                 const int last = run.pos(w.b) - s.own * kBlk, first = s.lo - s.own * kBlk;
                 if (warp * 16 <= last && warp * 16 + 15 >= first) {
-                    const size_t at = ((size_t)w.b * p.c.Hkv + kvh) * kBlkBytes;
-                    tail16<TK>(t, qt, p.scale_log2, reinterpret_cast<const TK*>(p.c.ktail) + at, p.c.vtail + at, warp * 16,
-                               first, last);
+                    Tail<TK> tail;
+                    tail.load(p, (size_t)w.b * p.c.Hkv + kvh, warp * 16);
+                    tail.take(t, qt, p.scale_log2, warp * 16, first, last);
                 }
             }
             const float2 qs = q_as_half<TK>(p, qt, q16);
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_
                     const float4 y = *reinterpret_cast<const float4*>(&sm.acc[h][d]);
                     const float o[4] = {y.x, y.y, y.z, y.w};
                     if (one) {
-                        finish4(p, head - r + h, d, m, l, o);
+                        finish4(p, head - r + h, d, m, l, o, load_gate(p, head - r + h, d));
                     } else {
                         float* rec = p.part + ((item + blockIdx.x) * p.rows + h) * DK_REC;
                         if (d == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
@@ -285,7 +285,10 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ D
     const int c0 = run_of(total, start), c1 = run_of(total, start + units - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");   // every block: the grid must not end before the records' writer
     if (c0 == c1 || ht * DK_HEADS + row >= p.G) return;
+    const size_t head = (size_t)b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS + row;
+    const uint2 gate = warp == 0 ? load_gate(p, head, 4 * lane) : make_uint2(0u, 0u);
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int c = c0 + warp; c <= c1; c += 4) {
         const float* rec = p.part + (((size_t)item + c) * p.rows + row) * DK_REC;
         const float2 x = *reinterpret_cast<const float2*>(rec);
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ D
         o[2] = fmaf(y.z, f, o[2]);
         o[3] = fmaf(y.w, f, o[3]);
     }
-    finish4(p, (size_t)b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS + row, 4 * lane, mm, l, o);
+    finish4(p, head, 4 * lane, mm, l, o, gate);
 }
 
 bool make_map(CUtensorMap* map, const void* codes, const Kv8& c) {

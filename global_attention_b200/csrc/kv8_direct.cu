@@ -5,7 +5,7 @@
 // There the whole call is a few microseconds, most of them latencies in a row: position, page number, codes.  So a
 // cluster of 1 to 8 CTAs takes an item whose units are split evenly among them; nothing but its own position
 // decides a CTA's work, the rows of q and of the tail load while page numbers do, the CTAs' parts meet in
-// shared memory across the cluster (each finishes a share of the dims), and there is no second kernel.  Four CTAs of
+// shared memory across the cluster (each is sent its share of all, and finishes it), and there is no second kernel.  Four CTAs of
 // four warps fit on an SM: their latencies overlap.
 #include <cooperative_groups.h>
 
@@ -19,14 +19,24 @@ namespace {
 constexpr int DD_THREADS = 128;
 constexpr int DD_WAIT = 0x820;
 constexpr size_t DD_RING = 4 * kSlots * kSlot;
-static_assert(DD_RING >= 5 * DK_HEADS * kD * sizeof(float), "the warps' parts and their sum take the ring's place");
+static_assert(DD_RING >= 4 * DK_HEADS * (kD + 4) * sizeof(float), "the warps' parts take the ring's place");
+
+constexpr int DD_ROW = kD + 4;   // floats of a head in a warp's part: the lanes' two heads in different banks
 
 struct DirectSmem {
     WarpSmem warp[4];
     float ml[4][DK_HEADS][2];
-    float cta_ml[DK_HEADS][2];
+    float from_ml[8][DK_HEADS][2];      // [CTA of the cluster]: its maximum and sum
+    float4 from[256];                   // [CTA][place of this CTA's share]: its O
     int abort;
 };
+
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename TK, int CODE>
 __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_constant__ DecodeKv8Params p) {
@@ -40,6 +50,15 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     const int nh = min(DK_HEADS, p.G - ht * DK_HEADS);
     const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS;
     const int pos = p.pos[b];
+    // What the position will ask for, into L2 while it is read: the sequence's page numbers, and for the first CTA the
+    // tail.
+    const size_t seq_head = (size_t)b * p.c.Hkv + kvh;
+    if (rank == 0 && lane < 2)
+        prefetch_l2(lane == 0 ? p.c.ktail + seq_head * kBlkBytes * 2 + warp * 16 * kD * 2
+                              : reinterpret_cast<const char*>(p.c.vtail + seq_head * kBlkBytes + warp * 16 * kD),
+                    16 * kD * 2);
+    if (warp == 3 && p.c.NB <= 2048)
+        for (int i = lane; i < (p.c.NB * 4 + 127) / 128; i += 32) prefetch_line(p.c.table + (size_t)b * p.c.NB + min(32 * i, p.c.NB - 1));
     uint32_t qt[8][2];
     load_q<TK>(p, head0 + r, r < nh, qt);
     if (lane == 0) {
@@ -48,13 +67,24 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         fence_barrier_init();
     }
     __syncthreads();
+    if (p.split > 1) cluster_arrive();   // this CTA's shared memory may be written to
     const Span s = span_of(p, pos);
     if (s.idle || s.bad) {   // the same for the whole cluster
         if (rank == 0 && warp == 0 && r < nh) no_answer(p, head0 + r, s.idle);
+        if (p.split > 1) cluster_wait();
         return;
     }
-    // this CTA's blocks, and of them this warp's pair's: every second one
-    const int n8 = s.units - 1, u0 = (int)((long long)n8 * rank / p.split), u1 = (int)((long long)n8 * (rank + 1) / p.split);
+    // this thread's places, of a head and 4 dims each: of 256, or of the CTA's share of them
+    const int share = 256 / p.split;
+    uint2 gate[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = rank * share + tid + DD_THREADS * i, h = at >> 5;
+        gate[i] = tid + DD_THREADS * i < share && h < nh ? load_gate(p, head0 + h, 4 * (at & 31)) : make_uint2(0u, 0u);
+    }
+    // this CTA's units, the tail the first of all; its blocks; of them this warp's pair's, every second one
+    const int u0 = max(0, (int)((long long)s.units * rank / p.split) - 1);
+    const int u1 = (int)((long long)s.units * (rank + 1) / p.split) - 1;
     const int team = warp >> 1, nt = (u1 - u0 - team + 1) / 2;
     Stream stream(p, sm.warp[warp], ring + warp * kSlots * kSlot, &sm.abort);
     auto fetch = [&](int batch) {   // lane i: the pair's block 32 batch + i
@@ -65,11 +95,12 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     stream.start(nt);
 
     State t;
-    if (rank == 0) {
+    if (rank == 0) {   // while the first codes are on their way
         const int last = pos - s.own * kBlk, first = s.lo - s.own * kBlk;
         if (warp * 16 <= last && warp * 16 + 15 >= first) {
-            const size_t at = ((size_t)b * p.c.Hkv + kvh) * kBlkBytes;
-            tail16<TK>(t, qt, p.scale_log2, reinterpret_cast<const TK*>(p.c.ktail) + at, p.c.vtail + at, warp * 16, first, last);
+            Tail<TK> tail;
+            tail.load(p, seq_head, warp * 16);
+            tail.take(t, qt, p.scale_log2, warp * 16, first, last);
         }
     }
     uint32_t q16[8][2];
@@ -80,10 +111,8 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         stream.take<CODE>(t, q16, qs, s.lo, k, nt, DD_WAIT, fetch);
     }
     stream.drain(gave_up, nt);
-
     // the warps' parts, in a fixed order; the ring is free once all have come here
-    float(*acc)[DK_HEADS][kD] = reinterpret_cast<float(*)[DK_HEADS][kD]>(ring);                      // [warp]
-    float(*sum)[kD] = reinterpret_cast<float(*)[kD]>(ring + 4 * DK_HEADS * kD * sizeof(float));      // the CTA's
+    float(*acc)[DK_HEADS][DD_ROW] = reinterpret_cast<float(*)[DK_HEADS][DD_ROW]>(ring);   // [warp]
     put_ml(t, sm.ml[warp]);
     __syncthreads();
     float m, l;
@@ -94,53 +123,55 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         *reinterpret_cast<float2*>(&acc[warp][2 * c][d]) = make_float2(t.o[i][0].x * fx, t.o[i][1].x * fx);
         *reinterpret_cast<float2*>(&acc[warp][2 * c + 1][d]) = make_float2(t.o[i][0].y * fy, t.o[i][1].y * fy);
     }
-    if (tid < DK_HEADS) {
-        join_ml(sm.ml, tid, 0, m, l);
-        sm.cta_ml[tid][0] = m;
-        sm.cta_ml[tid][1] = l;
-    }
     __syncthreads();
-    // 256 places of a head and 4 dims
-    float4 mine[2];
+    if (p.split > 1) cluster_wait();   // every CTA of the cluster runs
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int h = (tid + DD_THREADS * i) >> 5, d = 4 * (tid & 31);
-        mine[i] = *reinterpret_cast<const float4*>(&acc[0][h][d]);
+        const int at = tid + DD_THREADS * i, h = at >> 5, d = 4 * (at & 31);
+        float4 x = *reinterpret_cast<const float4*>(&acc[0][h][d]);
 #pragma unroll
         for (int w = 1; w < 4; ++w) {
             const float4 y = *reinterpret_cast<const float4*>(&acc[w][h][d]);
-            mine[i].x += y.x;
-            mine[i].y += y.y;
-            mine[i].z += y.z;
-            mine[i].w += y.w;
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
         if (p.split == 1) {
-            const float o[4] = {mine[i].x, mine[i].y, mine[i].z, mine[i].w};
-            if (h < nh) finish4(p, head0 + h, d, sm.cta_ml[h][0], sm.cta_ml[h][1], o);
-        } else {
-            *reinterpret_cast<float4*>(&sum[h][d]) = mine[i];
+            join_ml(sm.ml, h, 0, m, l);
+            const float o[4] = {x.x, x.y, x.z, x.w};
+            if (h < nh) finish4(p, head0 + h, d, m, l, o, gate[i]);
+        } else {   // to the CTA whose share the place is in
+            cluster.map_shared_rank(sm.from, at / share)[rank * share + at % share] = x;
         }
     }
     if (p.split > 1) {
-        cluster.sync();
-        const int share = 256 / p.split;   // at most one place of a thread
-        const int at = rank * share + tid, h = at >> 5, d = 4 * (at & 31);
-        if (tid < share && h < nh) {
-            float mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int i = 0; i < p.split; ++i) mm = fmaxf(mm, cluster.map_shared_rank(&sm, i)->cta_ml[h][0]);
-            for (int i = 0; i < p.split; ++i) {
-                const float* ml = cluster.map_shared_rank(&sm, i)->cta_ml[h];
-                const float4 y = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sum[h][d], i));
-                const float fi = ml[1] == 0.f ? 0.f : fast_exp2(ml[0] - mm);
-                ll = fmaf(ml[1], fi, ll);
-                o[0] = fmaf(y.x, fi, o[0]);
-                o[1] = fmaf(y.y, fi, o[1]);
-                o[2] = fmaf(y.z, fi, o[2]);
-                o[3] = fmaf(y.w, fi, o[3]);
-            }
-            finish4(p, head0 + h, d, mm, ll, o);
+        if (tid < DK_HEADS * p.split) {   // every CTA's copy of the maximum and sum
+            const int h = tid % DK_HEADS;
+            join_ml(sm.ml, h, 0, m, l);
+            *reinterpret_cast<float2*>(cluster.map_shared_rank(sm.from_ml, tid / DK_HEADS)[rank][h]) = make_float2(m, l);
         }
-        cluster.sync();   // shared memory that others read stays
+        cluster_arrive();
+        cluster_wait();
+        const int at = rank * share + tid, h = at >> 5;
+        if (tid < share && h < nh) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            m = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < p.split) m = fmaxf(m, sm.from_ml[i][h][0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < p.split) {
+                    const float2 ml = *reinterpret_cast<const float2*>(sm.from_ml[i][h]);
+                    const float4 y = sm.from[i * share + tid];
+                    const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
+                    l = fmaf(ml.y, f, l);
+                    o[0] = fmaf(y.x, f, o[0]);
+                    o[1] = fmaf(y.y, f, o[1]);
+                    o[2] = fmaf(y.z, f, o[2]);
+                    o[3] = fmaf(y.w, f, o[3]);
+                }
+            finish4(p, head0 + h, 4 * (at & 31), m, l, o, gate[0]);
+        }
     }
     if (tid == 0 && sm.abort) *p.err = sm.abort;
 }
@@ -169,7 +200,7 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
 bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
-    while (p.split < 8 && items * p.split * 2 <= 592 && units > 2 * p.split) p.split *= 2;
+    while (p.split < 8 && items * p.split * 2 <= 296 && units > 2 * p.split) p.split *= 2;
     return units <= 64 * p.split && items * p.split <= 0x7fffffffLL;
 }
 
