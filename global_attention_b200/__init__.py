@@ -120,7 +120,7 @@ def load() -> ctypes.CDLL:
         ll = ctypes.c_longlong
         lib.zgcm_kv8_append.argtypes = [cache, vp, ll, ll, ll, vp, ll, ll, ll, vp, vp, i, vp]
         lib.zgcm_kv8_append.restype = i
-        lib.zgcm_attn_decode_kv8_workspace_size.argtypes = [i, i, i]
+        lib.zgcm_attn_decode_kv8_workspace_size.argtypes = [cache, i, i, i]
         lib.zgcm_attn_decode_kv8_workspace_size.restype = sz
         lib.zgcm_attn_decode_kv8.argtypes = [cache, vp, vp, vp, vp, i, i, i, f, vp, vp, vp, sz, vp]
         lib.zgcm_attn_decode_kv8.restype = i
@@ -774,10 +774,10 @@ def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_bas
     if index < 0:
         raise TypeError("q must be a CUDA tensor")
     if qr is None:
-        qr = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        qr = q.new_empty((T, Hq, D), dtype=out_dtype)
         rqr = _Rows(qr.data_ptr(), Hq * D, D)
     if kr is None:
-        kr = torch.empty((T, Hkv, D), dtype=out_dtype, device=q.device)
+        kr = q.new_empty((T, Hkv, D), dtype=out_dtype)
         rkr = _Rows(kr.data_ptr(), Hkv * D, D)
     st = _run(index, stream, load().zgcm_qk_norm_rope_fwd, rq, rk, pgq, pgk, pp, T, Hq, Hkv, D, xt, yt, int(rope_dims),
               float(rope_base), float(eps), rqr, rkr)
@@ -812,17 +812,16 @@ def zgcm_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, dqr, dkr, *, rope_dims=42
     if index < 0:
         raise TypeError("q must be a CUDA tensor")
     if grads is None:
-        dev = q.device
-        dq, dk = torch.empty((T, Hq, D), dtype=q.dtype, device=dev), torch.empty((T, Hkv, D), dtype=q.dtype, device=dev)
-        dgq, dgk = torch.empty(D, dtype=torch.float32, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
+        dq, dk = q.new_empty((T, Hq, D)), k.new_empty((T, Hkv, D))
+        dgq, dgk = gamma_q.new_empty(D), gamma_k.new_empty(D)
         rdq, rdk = _Rows(dq.data_ptr(), Hq * D, D), _Rows(dk.data_ptr(), Hkv * D, D)
         pdgq, pdgk = dgq.data_ptr(), dgk.data_ptr()
         grads = {"dq": dq, "dk": dk, "dgamma_q": dgq, "dgamma_k": dgk}
     lib = load()
     if workspace is None:
-        workspace = torch.empty(max(16, lib.zgcm_qk_norm_rope_bwd_workspace_size(T)), dtype=torch.uint8, device=q.device)
+        workspace = gamma_q.new_empty(max(4, lib.zgcm_qk_norm_rope_bwd_workspace_size(T) // 4))
     st = _run(index, stream, lib.zgcm_qk_norm_rope_bwd, rq, rk, pgq, pgk, pp, rdqr, rdkr, T, Hq, Hkv, D, xt, yt,
-              int(rope_dims), float(rope_base), float(eps), rdq, rdk, pdgq, pdgk, workspace.data_ptr(), workspace.numel())
+              int(rope_dims), float(rope_base), float(eps), rdq, rdk, pdgq, pdgk, workspace.data_ptr(), workspace.nbytes)
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_qk_norm_rope_bwd")
     return grads
@@ -959,9 +958,11 @@ def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
     return cache
 
 
-def zgcm_attn_decode_kv8_workspace_size(n_seq, Hq, Hkv) -> int:
-    """Bytes of workspace zgcm_attn_decode_kv8 needs."""
-    return int(load().zgcm_attn_decode_kv8_workspace_size(int(n_seq), int(Hq), int(Hkv)))
+def zgcm_attn_decode_kv8_workspace_size(cache, Hq, *, window=128, n_list=None) -> int:
+    """Bytes of workspace zgcm_attn_decode_kv8 needs (n_list: the last dimension of `blocks`, if given)."""
+    _kv8_cache(cache)
+    return int(load().zgcm_attn_decode_kv8_workspace_size(cache._ref, int(Hq), _window(window),
+                                                          -1 if n_list is None else int(n_list)))
 
 
 def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=None, out=None, lse=None, workspace=None,
@@ -993,18 +994,21 @@ def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=Non
         _is(workspace, "workspace", torch.uint8, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else (), index)
     if index < 0:
         raise TypeError("q must be a CUDA tensor")
-    dev = cache.device
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = cache._t["v_tail"].new_empty(shape)
+    lib, window, fp32 = load(), _window(window), cache._t["k_scale"]
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    lib = load()
+        lse = fp32.new_empty((B, Hq))
+    pw, nw = None, 0
     if workspace is None:
-        workspace = torch.empty(max(16, lib.zgcm_attn_decode_kv8_workspace_size(B, Hq, cache.Hkv)), dtype=torch.uint8,
-                                device=dev)
-    st = _run(index, stream, lib.zgcm_attn_decode_kv8, cache._ref, pq, pg, pp, pb, n_list, Hq, _window(window),
-              1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-              workspace.numel())
+        nw = lib.zgcm_attn_decode_kv8_workspace_size(cache._ref, Hq, window, -1 if blocks is None else n_list)
+        if nw:
+            workspace = fp32.new_empty(nw // 4)
+            pw = workspace.data_ptr()
+    else:
+        pw, nw = workspace.data_ptr(), workspace.numel()
+    st = _run(index, stream, lib.zgcm_attn_decode_kv8, cache._ref, pq, pg, pp, pb, n_list, Hq, window,
+              1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), pw, nw)
     if st != ZGCM_OK:
         raise ZgcmError(st, "zgcm_attn_decode_kv8")
     return out, lse
@@ -1026,7 +1030,7 @@ def zgcm_kv8_select(cache, q, pos, n_select, *, n_first=1, n_last=1, window=128,
     if index < 0:
         raise TypeError("q must be a CUDA tensor")
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
+        out = cache._t["table"].new_empty(shape)
     st = _run(index, stream, load().zgcm_kv8_select, cache._ref, pq, pp, Hq, _window(window), n_select, int(n_first),
               int(n_last), out.data_ptr())
     if st != ZGCM_OK:

@@ -9,6 +9,7 @@
 // Bound by HBM for prompts (2 bytes read, 1 written per value) and by latency for single
 // tokens, which move one row per head and, every 64th token, a block.
 #include "kv8.cuh"
+#include "sm100.cuh"
 
 namespace zgcm {
 
@@ -72,25 +73,36 @@ template <> __device__ __forceinline__ float from_bits<__half>(uint32_t b) {
     return __half2float(__ushort_as_half((unsigned short)b));
 }
 
-// four codes of four values (x / scale, IEEE division: the code is that of the definition)
-template <int CODE> __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float scale) {
-    a = __fdiv_rn(a, scale);
-    b = __fdiv_rn(b, scale);
-    c = __fdiv_rn(c, scale);
-    d = __fdiv_rn(d, scale);
-    if (CODE == ZGCM_E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-        return lo | (hi << 16);
-    }
-    // |x / scale| <= 127 (1 + 2^-22) rounds to at most 127: no clamp
-    const int ia = __float2int_rn(a), ib = __float2int_rn(b), ic = __float2int_rn(c), id = __float2int_rn(d);
-    return (ia & 255) | ((ib & 255) << 8) | ((ic & 255) << 16) | ((uint32_t)(id & 255) << 24);
+// Two quotients x / s, correctly rounded: r = 1 / s rounded to nearest; x r is off by less than two units in the last
+// place, one step with the exact remainder x - q s brings it within one, and from there a second one gives the
+// nearest (Markstein, IBM J. Res. Dev. 34, 1990), as long as nothing underflows: s >= 2^-80 (kSmall; below it the division
+// operator).  An IEEE division by operator for each element was half of the kernel's instructions.
+constexpr float kSmall = 0x1p-80f;
+__device__ __forceinline__ float2 quotient(float2 x, float2 s, float2 minus_s, float2 r, bool small) {
+    if (small) return make_float2(__fdiv_rn(x.x, s.x), __fdiv_rn(x.y, s.y));
+    float2 q = sm100::fmul2(x, r);
+    q = sm100::ffma2(sm100::ffma2(minus_s, q, x), r, q);
+    return sm100::ffma2(sm100::ffma2(minus_s, q, x), r, q);
 }
 
-// largest magnitude (as the bits of a 16-bit type without its sign, which order like the
-// magnitudes, infinities and NaN above all finite ones) of the CTA's values
-__device__ __forceinline__ uint32_t cta_max_bits(const uint4 (&w)[AP_ROWS], uint32_t* red) {
+// four codes of four quotients
+template <int CODE> __device__ __forceinline__ uint32_t code4(float2 a, float2 b) {
+    if (CODE == ZGCM_E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+    // |x / scale| <= 127 (1 + 2^-22): in the last places of 1.5 2^23 it is rounded to nearest even, and its low byte is the code
+    const float2 m = make_float2(12582912.f, 12582912.f);
+    a = sm100::fadd2(a, m);
+    b = sm100::fadd2(b, m);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
+
+// largest magnitude of a thread's values, as the bits of a 16-bit type without its sign: they order like the
+// magnitudes, infinities and NaN above all finite ones
+__device__ __forceinline__ uint32_t max_bits(const uint4 (&w)[AP_ROWS]) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < AP_ROWS; ++i) {
@@ -99,14 +111,7 @@ __device__ __forceinline__ uint32_t cta_max_bits(const uint4 (&w)[AP_ROWS], uint
         m = __vmaxu2(m, w[i].z & 0x7fff7fffu);
         m = __vmaxu2(m, w[i].w & 0x7fff7fffu);
     }
-    m = max(m & 0xffffu, m >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = red[threadIdx.x & 7];
-    m = __reduce_max_sync(0xffffffffu, m);
-    __syncthreads();
-    return m;
+    return max(m & 0xffffu, m >> 16);
 }
 
 template <typename T, int CODE>
@@ -114,14 +119,17 @@ __device__ __forceinline__ void store_codes(const uint4 (&w)[AP_ROWS], uint32_t 
     const float amax = from_bits<T>(bits);
     const bool finite = isfinite(amax);
     const float scale = finite ? fmaxf(amax * (CODE == ZGCM_E4M3 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f) : NAN;
+    const float r = __frcp_rn(scale);
+    const float2 s2 = make_float2(scale, scale), m2 = make_float2(-scale, -scale), r2 = make_float2(r, r);
+    const bool small = scale < kSmall;
     const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < AP_ROWS; ++i) {
         uint2 y = make_uint2(0u, 0u);
         if (finite) {
-            const float2 a = unpack2<T>(w[i].x), b = unpack2<T>(w[i].y), c = unpack2<T>(w[i].z), d = unpack2<T>(w[i].w);
-            y.x = code4<CODE>(a.x, a.y, b.x, b.y, scale);
-            y.y = code4<CODE>(c.x, c.y, d.x, d.y, scale);
+            const float2 a = quotient(unpack2<T>(w[i].x), s2, m2, r2, small), b = quotient(unpack2<T>(w[i].y), s2, m2, r2, small);
+            const float2 c = quotient(unpack2<T>(w[i].z), s2, m2, r2, small), d = quotient(unpack2<T>(w[i].w), s2, m2, r2, small);
+            y = make_uint2(code4<CODE>(a, b), code4<CODE>(c, d));
         }
         *reinterpret_cast<uint2*>(codes + (row + 16 * i) * kD + 8 * col) = y;
     }
@@ -132,7 +140,7 @@ __device__ __forceinline__ void store_codes(const uint4 (&w)[AP_ROWS], uint32_t 
 // ones are in the tail
 template <typename TK, int CODE>
 __device__ __forceinline__ void do_block(const AppendParams& p, int b, int h, int j, int start, int end, int last,
-                                         uint32_t* red, float (*sum)[kD]) {
+                                         uint2* red, float (*sum)[kD]) {
     const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
     const int base = j * kBlk;
     const bool whole = end - base >= kBlk;
@@ -165,35 +173,37 @@ __device__ __forceinline__ void do_block(const AppendParams& p, int b, int h, in
     const int page = whole && j > last - p.c.NB ? kv8_page(p.c, b, j) : -1;
     if (page < 0) return;
     const size_t at = (size_t)page * p.c.Hkv + h;
-    store_codes<TK, CODE>(kw, cta_max_bits(kw, red), p.c.kc + at * kBlkBytes, p.c.ks + at);
-    store_codes<bf16, CODE>(vw, cta_max_bits(vw, red), p.c.vc + at * kBlkBytes, p.c.vs + at);
-    float m[8] = {};
+    uint32_t mk = __reduce_max_sync(0xffffffffu, max_bits(kw)), mv = __reduce_max_sync(0xffffffffu, max_bits(vw));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(mk, mv);
+    float2 m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < AP_ROWS; ++i) {
         const uint32_t u[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2<TK>(u[e]);
-            m[2 * e] += f.x;
-            m[2 * e + 1] += f.y;
-        }
+        for (int e = 0; e < 4; ++e) m[e] = sm100::fadd2(m[e], unpack2<TK>(u[e]));
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[row][8 * col + e] = m[e];
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(&sum[row][8 * col + 2 * e]) = m[e];
     __syncthreads();
+    const uint2 all = red[threadIdx.x & 7];
+    mk = __reduce_max_sync(0xffffffffu, all.x);
+    mv = __reduce_max_sync(0xffffffffu, all.y);
+    store_codes<TK, CODE>(kw, mk, p.c.kc + at * kBlkBytes, p.c.ks + at);
+    store_codes<bf16, CODE>(vw, mv, p.c.vc + at * kBlkBytes, p.c.vs + at);
     if (threadIdx.x < kD) {
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < AP_THREADS / 16; ++i) a += sum[i][threadIdx.x];
         reinterpret_cast<TK*>(p.c.kmean)[at * kD + threadIdx.x] = TK(a * (1.0f / kBlk));
     }
-    __syncthreads();
 }
 
 // grid (blocks of the longest possible sequence, KV heads, sequences)
 template <typename TK, int CODE>
 __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ uint32_t red[8];
+    __shared__ uint2 red[8];
     __shared__ __align__(16) float sum[AP_THREADS / 16][kD];
     const int b = blockIdx.z, h = blockIdx.y;
     const int start = p.pos[b];
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const __grid_con
     if (j > last || (j == last && j != first)) return;
     do_block<TK, CODE>(p, b, h, j, start, end, last, red, sum);
     if (j == first && last != first) {
-        __syncthreads();   // the tail's old rows have been read
+        __syncthreads();   // the tail's old rows, red and sum have been read
         do_block<TK, CODE>(p, b, h, last, start, end, last, red, sum);
     }
 }

@@ -362,6 +362,29 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
     return cudaLaunchKernelEx(&cfg, kv8_join_kernel, p);
 }
 
+// Checks and the shape-dependent part of the parameters; n_list < 0: no list.
+int plan(DecodeKv8Params& p, const zgcm_kv8_cache* cache, int Hq, int window, int n_list, bool* direct) {
+    const int st = kv8_check(cache, &p.c);
+    if (st != ZGCM_OK) return st;
+    if (Hq < 1 || Hq % p.c.Hkv != 0 || window < 1) return ZGCM_ERR_INVALID_ARG;
+    p.n_list = n_list < 0 ? 0 : n_list;
+    p.Hq = Hq;
+    p.G = Hq / p.c.Hkv;
+    p.HT = (p.G + DK_HEADS - 1) / DK_HEADS;
+    p.rows = p.G < DK_HEADS ? p.G : DK_HEADS;
+    p.W = window;
+    // items and their heads are counted in 32 bits (grids and records; 8 CTAs of an item)
+    if ((long long)p.c.B * p.c.Hkv * p.HT * DK_HEADS > 0x7fffffffLL || n_list > 0x7ffffffe) return ZGCM_ERR_UNSUPPORTED;
+    // the most units of an item: a list's entries, or the blocks that a window can touch and the table hold
+    const long long touched = ((long long)window - 1 + kBlk - 1) / kBlk + 1;
+    *direct = kv8_direct_plan(p, n_list >= 0 ? n_list + 1 : (int)(touched < p.c.NB ? touched : p.c.NB));
+    return ZGCM_OK;
+}
+
+size_t records_bytes(const DecodeKv8Params& p) {
+    return ((size_t)p.c.B * p.c.Hkv * p.HT + DK_CTAS) * p.rows * DK_REC * sizeof(float);
+}
+
 }  // namespace
 }  // namespace zgcm
 
@@ -369,50 +392,44 @@ using namespace zgcm;
 
 extern "C" {
 
-size_t zgcm_attn_decode_kv8_workspace_size(int n_seq, int Hq, int Hkv) {
-    if (n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
-    const int G = Hq / Hkv, HT = (G + DK_HEADS - 1) / DK_HEADS, rows = G < DK_HEADS ? G : DK_HEADS;
-    return ((size_t)n_seq * Hkv * HT + DK_CTAS) * rows * DK_REC * sizeof(float);
+size_t zgcm_attn_decode_kv8_workspace_size(const zgcm_kv8_cache* cache, int Hq, int window, int n_list) {
+    DecodeKv8Params p;
+    bool direct;
+    if (plan(p, cache, Hq, window, n_list < 0 ? -1 : n_list, &direct) != ZGCM_OK || p.c.B == 0 || direct) return 0;
+    return records_bytes(p);
 }
 
 int zgcm_attn_decode_kv8(const zgcm_kv8_cache* cache, const void* q, const void* g, const int* pos, const int* blocks,
                          int n_list, int Hq, int window, float scale, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, void* cuda_stream) {
     DecodeKv8Params p;
-    const int st = kv8_check(cache, &p.c);
+    bool direct;
+    if (blocks && n_list < 0) return ZGCM_ERR_INVALID_ARG;
+    const int st = plan(p, cache, Hq, window, blocks ? n_list : -1, &direct);
     if (st != ZGCM_OK) return st;
-    if (Hq < 1 || Hq % p.c.Hkv != 0 || window < 1 || (blocks && n_list < 0)) return ZGCM_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !isfinite(scale)) return ZGCM_ERR_INVALID_ARG;
     if (p.c.B == 0) return ZGCM_OK;
     if (!q || !pos || !out || !lse) return ZGCM_ERR_INVALID_ARG;
     if (((uintptr_t)q | (uintptr_t)g | (uintptr_t)pos | (uintptr_t)blocks | (uintptr_t)out | (uintptr_t)lse) & 15u)
         return ZGCM_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < zgcm_attn_decode_kv8_workspace_size(p.c.B, Hq, p.c.Hkv)) return ZGCM_ERR_WORKSPACE;
-    if ((uintptr_t)workspace & 15u) return ZGCM_ERR_ALIGNMENT;
+    if (!direct) {
+        if (!workspace || workspace_bytes < records_bytes(p)) return ZGCM_ERR_WORKSPACE;
+        if ((uintptr_t)workspace & 15u) return ZGCM_ERR_ALIGNMENT;
+    }
     p.q = q;
     p.g = static_cast<const bf16*>(g);
     p.pos = pos;
     p.blocks = blocks;
-    p.n_list = blocks ? n_list : 0;
-    p.Hq = Hq;
-    p.G = Hq / p.c.Hkv;
-    p.HT = (p.G + DK_HEADS - 1) / DK_HEADS;
-    p.rows = p.G < DK_HEADS ? p.G : DK_HEADS;
-    p.W = window;
     p.scale_log2 = scale * kLog2e;
     p.out = static_cast<bf16*>(out);
     p.lse = lse;
     p.part = static_cast<float*>(workspace);
     p.err = library_error_word();
-    // items are counted in 32 bits (grids and records)
-    if (!p.err || (long long)p.c.B * p.c.Hkv * p.HT * p.rows > 0x7fffffffLL) return ZGCM_ERR_UNSUPPORTED;
+    if (!p.err) return ZGCM_ERR_CUDA;
     if (!make_map(&p.tm_k, p.c.kc, p.c) || !make_map(&p.tm_v, p.c.vc, p.c)) return ZGCM_ERR_CUDA;
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     const bool f8 = p.c.code == ZGCM_E4M3;
-    // the most units of an item: a list's entries, or the blocks that a window can touch and the table hold
-    const long long touched = ((long long)window - 1 + kBlk - 1) / kBlk + 1;
-    if (kv8_direct_plan(p, blocks ? p.n_list + 1 : (int)(touched < p.c.NB ? touched : p.c.NB)))
-        return kv8_direct_launch(p, stream) == cudaSuccess ? ZGCM_OK : ZGCM_ERR_CUDA;
+    if (direct) return kv8_direct_launch(p, stream) == cudaSuccess ? ZGCM_OK : ZGCM_ERR_CUDA;
     const cudaError_t e = p.c.key == ZGCM_BF16
                               ? (f8 ? launch<bf16, ZGCM_E4M3>(p, stream) : launch<bf16, ZGCM_INT8>(p, stream))
                               : (f8 ? launch<__half, ZGCM_E4M3>(p, stream) : launch<__half, ZGCM_INT8>(p, stream));

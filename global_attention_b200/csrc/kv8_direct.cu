@@ -201,7 +201,7 @@ bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
     while (p.split < 8 && items * p.split * 2 <= 296 && units > 2 * p.split) p.split *= 2;
-    return units <= 64 * p.split && items * p.split <= 0x7fffffffLL;
+    return units <= 64 * p.split;
 }
 
 cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream) {

@@ -86,10 +86,11 @@ int zgcm_kv8_append(const zgcm_kv8_cache* cache, const void* k, long long k_b_st
  * q [n_seq, Hq, D] key_type; g [n_seq, Hq, D] bf16, or NULL for no gate (out = the softmax's
  * mean); out bf16 [n_seq, Hq, D]; lse fp32 [n_seq, Hq].  Idle sequences: out 0, lse -inf.
  * A window that reaches further back than n_blocks blocks (the own one among them): NaN.
- * workspace: zgcm_attn_decode_kv8_workspace_size bytes, 16-byte aligned, contents on entry
- * irrelevant, not used by a concurrent call.
+ * workspace: zgcm_attn_decode_kv8_workspace_size bytes (n_list < 0: no list), 16-byte aligned, contents on
+ * entry irrelevant, not used by a concurrent call.  0, and workspace may be NULL, where no sequence can have many blocks to
+ * read, and for arguments that zgcm_attn_decode_kv8 rejects; positions do not matter.
  */
-size_t zgcm_attn_decode_kv8_workspace_size(int n_seq, int Hq, int Hkv);
+size_t zgcm_attn_decode_kv8_workspace_size(const zgcm_kv8_cache* cache, int Hq, int window, int n_list);
 
 int zgcm_attn_decode_kv8(const zgcm_kv8_cache* cache, const void* q, const void* g, const int* pos, const int* blocks,
                          int n_list, int Hq, int window, float scale, void* out, float* lse, void* workspace,

@@ -59,8 +59,7 @@ def _decode(lib, cache=None, bad=None, ptr=0, n_list=0, Hq=8, window=128, scale=
     p = [P0 + 2 ** 20 + 4096 * i for i in range(6)]   # q, g, pos, blocks, out, lse
     if bad is not None:
         p[bad] = ptr
-    need = lib.zgcm_attn_decode_kv8_workspace_size(2, Hq, 2)
-    w, wb = (P0 + 2 ** 24, need) if ws is None else ws
+    w, wb = (P0 + 2 ** 24, 2 ** 30) if ws is None else ws
     return lib.zgcm_attn_decode_kv8(_cache() if cache is None else cache, *(vp(x) for x in p[:4]), n_list, Hq, window, scale,
                                     *(vp(x) for x in p[4:]), vp(w), wb, None)
 
@@ -108,11 +107,18 @@ def test_refuses_decode(lib):
         assert _decode(lib, bad=i, ptr=P0 + 4) == -3
     for kw in (dict(Hq=0), dict(Hq=7), dict(window=0), dict(scale=0.0), dict(scale=float("nan")), dict(n_list=-1)):
         assert _decode(lib, ws=(P0, 2 ** 40), **kw) == -1, kw
-    need = lib.zgcm_attn_decode_kv8_workspace_size(2, 8, 2)
-    assert need > 0 and _decode(lib, ws=(P0, need - 1)) == -4 and _decode(lib, ws=(0, need)) == -4
-    assert _decode(lib, ws=(P0 + 8, need)) == -3
+    # many blocks (150000 tokens of two sequences, or a list of that many): records of 2 x 2 items and 592 CTAs, 4 heads
     size = lib.zgcm_attn_decode_kv8_workspace_size
-    assert size(0, 8, 2) == size(2, 7, 2) == size(2, 8, 0) == 0
+    big, need = dict(n_blocks=2400), (2 * 2 + 592) * 4 * 132 * 4
+    assert size(_cache(**big), 8, 10 ** 6, -1) == size(_cache(), 8, 128, 2400) == need
+    for kw in (dict(cache=_cache(**big), window=10 ** 6), dict(n_list=2400)):
+        if "n_list" not in kw:
+            kw.update(bad=3, ptr=0)   # no list
+        assert _decode(lib, ws=(P0, need - 1), **kw) == -4 and _decode(lib, ws=(0, need), **kw) == -4
+        assert _decode(lib, ws=(P0 + 8, need), **kw) == -3
+    # few blocks by the window, by the list or by the table: none
+    assert size(_cache(**big), 8, 128, -1) == size(_cache(**big), 8, 10 ** 6, 32) == size(_cache(), 8, 10 ** 6, -1) == 0
+    assert size(_cache(**big), 7, 10 ** 6, -1) == size(_cache(n_seq=0, **big), 8, 10 ** 6, -1) == 0
     assert _decode(lib, _cache(n_seq=0)) == 0
 
 
@@ -254,8 +260,8 @@ def _check_held(c, k, v, code, lens=None, upto=None):
                         x64 = blk.double()
                         m = cpu["k_mean"][page, h].double()
                         tol = torch.finfo(k.dtype).eps / 2 * x64.mean(0).abs() * 1.001 + 20 * 2.0 ** -24 * x64.abs().mean(0)
-                        if k.dtype == torch.float16:
-                            tol += 2.0 ** -25
+                        # below the type's normal numbers: half its smallest step
+                        tol += 2.0 ** -25 if k.dtype == torch.float16 else 2.0 ** -134
                         assert ((m - x64.mean(0)).abs() <= tol).all()
         n = S - last * 64
         for side, x in (("k", k), ("v", v)):
@@ -655,7 +661,7 @@ def test_graphs_follow_positions(cuda):
     for c in caches:
         _feed(c, k[:, :190], v[:, :190], [190])
     q, g = _queries(B, Hq, "bf16")
-    ws = torch.empty(ga.zgcm_attn_decode_kv8_workspace_size(B, Hq, Hkv), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(2 ** 20, dtype=torch.uint8, device="cuda")
     qd, gd, kd, vd = q.cuda(), g.cuda(), k.cuda(), v.cuda()
     st = dict(k=kd[:, 190:191].clone(), v=vd[:, 190:191].clone(), pos=_i32(190, 190))
 
@@ -722,3 +728,30 @@ def test_shared_prefix_pages(cuda):
     _feed(c, k[:, 128:], v[:, 128:], [72], start=128)
     q, g = _queries(2, 4, "bf16")
     _check_decode(c, k, v, q, g, "e4m3")
+
+
+@gpu
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("key", ["bf16", "fp16"])
+def test_codes_of_every_mantissa(cuda, code, key):
+    """Quotients at and next to the middle between two codes: every significand of three binades against largest
+    magnitudes of many kinds (those that put ties exactly on 16-bit values among them), down to where the scale is its
+    smallest."""
+    bits = 7 if key == "bf16" else 10
+    g = torch.Generator().manual_seed(4)
+    # a head's 64 x 128 values; heads 0 .. 39: largest magnitudes 1 .. 2, 448 / 256 and 127 / 64 among them
+    tops = torch.cat([1 + torch.arange(0, 32) / 32, torch.tensor([1.75, 127 / 64, 448 / 256 * 0.875, 1.0625]),
+                      1 + torch.rand(4, generator=g)])
+    shift = 2.0 ** (1 - torch.randint(0, 9, (64, 128), generator=g).double())
+    sig = 1 + (torch.arange(64 * 128) % 2 ** bits).view(64, 128).double() / 2 ** bits
+    sign = torch.where(torch.rand(64, 128, generator=g) < 0.5, -1.0, 1.0)
+    x = (sig * shift * sign).unsqueeze(1).repeat(1, 40, 1)
+    for down in (1.0, 2.0 ** -10, 2.0 ** -100, 2.0 ** -118, 2.0 ** -124) if key == "bf16" else (1.0, 2.0 ** -8, 2.0 ** 12):
+        t = (tops.to(KEY[key]).double() * 2).view(1, 40, 1)
+        y = torch.where(x.abs() > t, x / 4, x)
+        y[0, :, 0] = t[0, :, 0]
+        k = (y * down).to(KEY[key]).unsqueeze(0)
+        v = (y.flip(0) * (down if key == "bf16" else 1.0)).to(torch.bfloat16).unsqueeze(0)
+        c = _new(1, 2, 40, code, key)
+        _feed(c, k, v, [64])
+        _check_held(c, k, v, code)

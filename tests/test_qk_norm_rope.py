@@ -71,11 +71,13 @@ def test_refuses_pointers(lib, bwd):
 
 def test_workspace(lib):
     size = lib.zgcm_qk_norm_rope_bwd_workspace_size
-    assert size(0) == 0 and size(-3) == 0 and size(1) == 1024
-    assert size(10 ** 6) == 592 * 1024
-    assert _c(lib, True, ws=(P, 4 * 1024 - 1)) == -4
-    assert _c(lib, True, ws=(0, 4 * 1024)) == -4
-    assert _c(lib, True, ws=(P + 8, 4 * 1024)) == -3
+    # 1 KB for each CTA: 2 for a token (16 warps share its rows), at most 296
+    assert size(0) == 0 and size(-3) == 0 and size(1) == 2 * 1024
+    assert size(10 ** 6) == 296 * 1024
+    need = size(4)
+    assert _c(lib, True, ws=(P, need - 1)) == -4
+    assert _c(lib, True, ws=(0, need)) == -4
+    assert _c(lib, True, ws=(P + 8, need)) == -3
 
 
 def test_empty_forward_launches_nothing(lib):
