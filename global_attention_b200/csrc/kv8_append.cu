@@ -75,11 +75,10 @@ template <> __device__ __forceinline__ float from_bits<__half>(uint32_t b) {
 
 // Two quotients x / s, correctly rounded: r = 1 / s rounded to nearest; x r is off by less than two units in the last
 // place, one step with the exact remainder x - q s brings it within one, and from there a second one gives the
-// nearest (Markstein, IBM J. Res. Dev. 34, 1990), as long as nothing underflows: s >= 2^-80 (kSmall; below it the division
-// operator).  An IEEE division by operator for each element was half of the kernel's instructions.
-constexpr float kSmall = 0x1p-80f;
-__device__ __forceinline__ float2 quotient(float2 x, float2 s, float2 minus_s, float2 r, bool small) {
-    if (small) return make_float2(__fdiv_rn(x.x, s.x), __fdiv_rn(x.y, s.y));
+// nearest (Markstein, IBM J. Res. Dev. 34, 1990), as long as nothing underflows: a block of smallest values is first
+// multiplied by 2^100 (`up`, else 1), x and s alike.  (The division operator was half of the kernel's instructions.)
+__device__ __forceinline__ float2 quotient(float2 x, float2 up, float2 minus_s, float2 r) {
+    x = sm100::fmul2(x, up);
     float2 q = sm100::fmul2(x, r);
     q = sm100::ffma2(sm100::ffma2(minus_s, q, x), r, q);
     return sm100::ffma2(sm100::ffma2(minus_s, q, x), r, q);
@@ -118,22 +117,19 @@ template <typename T, int CODE>
 __device__ __forceinline__ void store_codes(const uint4 (&w)[AP_ROWS], uint32_t bits, uint8_t* codes, float* scale_out) {
     const float amax = from_bits<T>(bits);
     const bool finite = isfinite(amax);
-    const float scale = finite ? fmaxf(amax * (CODE == ZGCM_E4M3 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f) : NAN;
-    const float r = __frcp_rn(scale);
-    const float2 s2 = make_float2(scale, scale), m2 = make_float2(-scale, -scale), r2 = make_float2(r, r);
-    const bool small = scale < kSmall;
+    const float scale = fmaxf(amax * (CODE == ZGCM_E4M3 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f);
+    const float up = scale < 0x1p-80f ? 0x1p100f : 1.f, s = scale * up, r = __frcp_rn(s);
+    const float2 u2 = make_float2(up, up), m2 = make_float2(-s, -s), r2 = make_float2(r, r);
     const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < AP_ROWS; ++i) {
-        uint2 y = make_uint2(0u, 0u);
-        if (finite) {
-            const float2 a = quotient(unpack2<T>(w[i].x), s2, m2, r2, small), b = quotient(unpack2<T>(w[i].y), s2, m2, r2, small);
-            const float2 c = quotient(unpack2<T>(w[i].z), s2, m2, r2, small), d = quotient(unpack2<T>(w[i].w), s2, m2, r2, small);
-            y = make_uint2(code4<CODE>(a, b), code4<CODE>(c, d));
-        }
+        const float2 a = quotient(unpack2<T>(w[i].x), u2, m2, r2), b = quotient(unpack2<T>(w[i].y), u2, m2, r2);
+        const float2 c = quotient(unpack2<T>(w[i].z), u2, m2, r2), d = quotient(unpack2<T>(w[i].w), u2, m2, r2);
+        uint2 y = make_uint2(code4<CODE>(a, b), code4<CODE>(c, d));
+        if (!finite) y = make_uint2(0u, 0u);
         *reinterpret_cast<uint2*>(codes + (row + 16 * i) * kD + 8 * col) = y;
     }
-    if (threadIdx.x == 0) *scale_out = scale;
+    if (threadIdx.x == 0) *scale_out = finite ? scale : NAN;
 }
 
 // block j of KV head h of sequence b: positions [lo, hi) of it are new (lo >= start), earlier
@@ -202,7 +198,7 @@ __device__ __forceinline__ void do_block(const AppendParams& p, int b, int h, in
 
 // grid (blocks of the longest possible sequence, KV heads, sequences)
 template <typename TK, int CODE>
-__global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(AP_THREADS, 4) kv8_append_kernel(const __grid_constant__ AppendParams p) {
     __shared__ uint2 red[8];
     __shared__ __align__(16) float sum[AP_THREADS / 16][kD];
     const int b = blockIdx.z, h = blockIdx.y;
@@ -212,10 +208,11 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const __grid_con
     const int end = start + n, first = start / kBlk, last = (end - 1) / kBlk;
     const int j = first + (int)blockIdx.x;
     if (j > last || (j == last && j != first)) return;
-    do_block<TK, CODE>(p, b, h, j, start, end, last, red, sum);
-    if (j == first && last != first) {
+#pragma unroll 1
+    for (int at = j;; at = last) {
+        do_block<TK, CODE>(p, b, h, at, start, end, last, red, sum);
+        if (j != first || at == last) break;
         __syncthreads();   // the tail's old rows, red and sum have been read
-        do_block<TK, CODE>(p, b, h, last, start, end, last, red, sum);
     }
 }
 
