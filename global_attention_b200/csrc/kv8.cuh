@@ -27,7 +27,7 @@ struct Kv8 {
 
 // page of block j of sequence b, or -1 when the table holds a number outside the cache
 __device__ __forceinline__ int kv8_page(const Kv8& c, int b, int j) {
-    const int p = c.table[(size_t)b * c.NB + j % c.NB];
+    const int p = c.table[(size_t)b * c.NB + (j < c.NB ? j : j % c.NB)];   // a ring's blocks alone pay for the division
     return (unsigned)p < (unsigned)c.P ? p : -1;
 }
 

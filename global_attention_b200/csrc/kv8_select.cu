@@ -4,34 +4,34 @@
 //   score_j = max over the KV head's queries of q . k_mean_j;  the n_select highest, ties to
 //   the lowest block, in ascending order.
 //
-// One pass over the block means, 256 bytes each.  The sums run in fp64: products of 16-bit
-// values are exact there and the sum of 128 of them is off by 2^-46 of its terms at most, so the
-// choice is that of the exact scores for all but astronomically close ties, and does not
-// depend on the order of the sum.  They go to the fp64 matrix instruction, 8 blocks by 8 heads by 4 dims: a lane
-// holds a quarter of a block's mean, one run of 64 bytes, and converts each element once for all heads (as sums
-// by lanes and shuffles the scores took three times the instructions, and the kernel was bound by them).
+// One pass over the block means, 256 bytes each.  The choice is that of fp64 sums (products of 16-bit values
+// are exact there and the sum of 128 of them is off by 2^-46 of its terms at most), but only blocks at the border
+// need them: the tensor cores give every score in fp32 (16 blocks by 8 heads an instruction), off by less than
+//      eps = 2^-13 max_h |q_h|_1 max_j |k_mean_j|_max
+// (8 sums of 17 terms, each off by 2^-22 of the largest of them at most: 2^-14.9 of the terms' sum); one histogram of 1024
+// equal steps finds the step that holds the need-th highest of them, between v0 and v1 as it turns out; what lies above
+// v1 + 2 eps is taken, what lies below v0 - 2 eps is not, and the few between are scored in fp64 and ranked by
+// counting.  (All scores in fp64, on the fp64 matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for either
+// of the benchmark's shapes against NNN.)  Where more than 256 are between, many equal scores say, or a score
+// is not finite, all are scored in fp64 and the histogram is taken of those (as ordered 64-bit integers), as often as one step
+// of it holds too many.
 //
-// A cluster of CTAs takes one (sequence, KV head): each scores a slice of the blocks and writes
-// its keys (fp64 scores as ordered 64-bit integers) into the first CTA's shared memory, which finds the
-// n-th highest: up to 64 keys by counting, for each, those above it; more by one histogram of 1024 equal steps between
-// the lowest and the highest, counting then among the few keys of the step the n-th falls in (or
-// another histogram of that step, where they are many).  One scan writes the list in order.
+// A cluster of CTAs takes one (sequence, KV head): each scores a slice of the blocks and writes the scores into
+// the first CTA's shared memory, which does the rest.
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include "kv8.cuh"
+#include "kv8_attn.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace zgcm {
 namespace {
 
-constexpr int SEL_ROWS = 8;                       // blocks of a warp at a time
-constexpr int SEL_HEADS = 8;                      // heads at a time
-constexpr int SEL_AHEAD = 4;                      // steps of a warp whose page numbers are looked up together
+constexpr int SEL_ROWS = 16;                      // blocks of a warp at a time
+constexpr int SEL_AHEAD = 2;                      // steps of a warp whose page numbers are looked up together
 constexpr int SEL_BITS = 10, SEL_BINS = 1 << SEL_BITS;
-constexpr int SEL_LIST = 256;                     // most keys of a step ranked by counting
-constexpr int SEL_FEW = 64;                       // most keys ranked by counting without a histogram
+constexpr int SEL_LIST = 256;                     // most keys ranked by counting
 
 struct SelectParams {
     Kv8 c;
@@ -48,12 +48,17 @@ __device__ __forceinline__ u64 ordered(double x) {
     return b < 0 ? ~(u64)b : (u64)b | (1ULL << 63);
 }
 
-// d += A B for 8 x 4 and 4 x 8: a of row lane / 4 and column lane % 4, b of row lane % 4 and column lane / 4, d of row
-// lane / 4 and columns 2 (lane % 4), + 1
-__device__ __forceinline__ void mma_f64(double (&d)[2], double a, double b) {
-    asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
-                 : "+d"(d[0]), "+d"(d[1])
-                 : "d"(a), "d"(b));
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return (int)b < 0 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) { return __uint_as_float((int)k < 0 ? k & 0x7fffffffu : ~k); }
+
+// the value of a 16-bit type's magnitude bits
+template <typename T> __device__ __forceinline__ float magnitude(uint32_t bits);
+template <> __device__ __forceinline__ float magnitude<bf16>(uint32_t bits) { return __uint_as_float(bits << 16); }
+template <> __device__ __forceinline__ float magnitude<__half>(uint32_t bits) {
+    return __half2float(__ushort_as_half((unsigned short)bits));
 }
 
 // exclusive scan over the CTA; every thread calls it
@@ -76,17 +81,17 @@ template <int WARPS> __device__ __forceinline__ uint32_t cta_scan(uint32_t x, ui
 }
 
 struct SelSmem {
-    double q[32][4][SEL_HEADS];   // [dim of a quarter][quarter][head]
     uint32_t hist[SEL_BINS];
     u64 list[SEL_LIST];
-    u64 lo[16], hi[16];           // lowest and highest key of each warp's
+    uint16_t index[SEL_LIST];     // of the list's keys
+    u64 lo[16], hi[16];           // lowest and highest of each warp's
     u64 thr;                      // keys above it are taken, and `need_eq` of those equal to it, the first ones
     uint32_t red[16];
-    uint32_t bin, above, count, n_list, need_eq;
+    uint32_t bin, above, count, n_list, need_eq, taken;
+    uint32_t mean_max;            // largest |k_mean| as its bits, q's largest 1-norm as fp32 bits
+    uint32_t q1;
+    uint32_t v0, v1;              // ordered
 };
-
-// Key number i of n as one of those that compete: not the first n_first nor the last n_last
-__device__ __forceinline__ bool forced(const SelectParams& p, int i, int n) { return i < p.n_first || i >= n - p.n_last; }
 
 // sm.thr and sm.need_eq of the `need` highest keys of the list (n <= SEL_LIST of them, at least `need`)
 __device__ __forceinline__ void rank_list(SelSmem& sm, int n, int need) {
@@ -107,22 +112,82 @@ __device__ __forceinline__ void rank_list(SelSmem& sm, int n, int need) {
     __syncthreads();
 }
 
+// The step of the histogram, counted from the top, in which the need-th falls: sm.bin, its sm.count and the number
+// sm.above of those in higher steps.  The histogram is left zeroed.
+template <int THREADS> __device__ __forceinline__ void find_step(SelSmem& sm, int need) {
+    constexpr int PER = SEL_BINS / THREADS;
+    const int tid = threadIdx.x;
+    uint32_t c[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        uint32_t& h = sm.hist[SEL_BINS - 1 - (tid * PER + i)];
+        c[i] = h;
+        h = 0;
+        mine += c[i];
+    }
+    uint32_t before = cta_scan<THREADS / 32>(mine, sm.red);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (before < (uint32_t)need && before + c[i] >= (uint32_t)need) {
+            sm.bin = SEL_BINS - 1 - (tid * PER + i);
+            sm.above = before;
+            sm.count = c[i];
+        }
+        before += c[i];
+    }
+    __syncthreads();
+}
+
+// The fp64 score of block `row` (counted from jlo) as an ordered integer, by a warp: -inf for a bad page or a NaN.
+template <typename TK>
+__device__ __forceinline__ u64 exact_key(const SelectParams& p, int b, int kvh, int j) {
+    const int lane = threadIdx.x & 31, G = p.Hq / p.c.Hkv;
+    const int page = kv8_page(p.c, b, j);
+    if (page < 0) return ordered(-INFINITY);
+    const TK* m = reinterpret_cast<const TK*>(p.c.kmean) + ((size_t)page * p.c.Hkv + kvh) * kD + 4 * lane;
+    double x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (double)key_to_float(m[e]);
+    double best = -INFINITY;
+    bool nan = false;
+    for (int h = 0; h < G; ++h) {
+        const TK* q = static_cast<const TK*>(p.q) + ((size_t)b * p.Hq + (size_t)kvh * G + h) * kD + 4 * lane;
+        double a = 0.0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a = fma((double)key_to_float(q[e]), x[e], a);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        nan |= isnan(a);
+        best = a > best ? a : best;
+    }
+    return ordered(nan ? -INFINITY : best);
+}
+
 template <typename TK, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int WARPS = THREADS / 32;
     extern __shared__ __align__(16) unsigned char dyn[];
     SelSmem& sm = *reinterpret_cast<SelSmem*>(dyn);
-    u64* key = reinterpret_cast<u64*>(dyn + sizeof(SelSmem));   // [candidates]; as doubles until they are sent
-    double* score = reinterpret_cast<double*>(key);
+    float* score = reinterpret_cast<float*>(dyn + sizeof(SelSmem));   // [candidates], of the first CTA
+    u64* key = reinterpret_cast<u64*>(dyn + sizeof(SelSmem));         // the same place, where fp64 scores take over
     cg::cluster_group cluster = cg::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
     const int item = blockIdx.x / cs, b = item / p.c.Hkv, kvh = item % p.c.Hkv;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int G = p.Hq / p.c.Hkv;
     const int pos = p.pos[b];
     // the sequence's page numbers into L2 while its position is read
     for (int i = tid; i < (p.c.NB * 4 + 127) / 128; i += THREADS)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.table + (size_t)b * p.c.NB + min(32 * i, p.c.NB - 1)));
+    for (int i = tid; i < SEL_BINS; i += THREADS) sm.hist[i] = 0;
+    if (tid == 0) {
+        sm.mean_max = sm.q1 = 0;
+        sm.n_list = sm.taken = 0;
+        sm.v0 = ~0u;
+        sm.v1 = 0u;
+        sm.thr = ~0ULL;
+        sm.need_eq = 0;
+    }
     const int own = pos < 0 ? 0 : pos / kBlk, jlo = pos < 0 ? 0 : max(0, pos - p.W + 1) / kBlk;
     const bool reach = own - jlo < p.c.NB;        // the window's blocks are all in the table
     const int n = reach ? own - jlo : 0;          // candidates jlo .. own - 1
@@ -132,108 +197,188 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
             for (int i = tid; i < p.n_select; i += THREADS) out[i] = i < n ? jlo + i : -1;
         return;
     }
-    for (int i = tid; i < SEL_BINS; i += THREADS) sm.hist[i] = 0;
-    const int per = (n + cs - 1) / cs, r0 = min(n, rank * per), r1 = min(n, r0 + per);
-    for (int h0 = 0; h0 < G; h0 += SEL_HEADS) {
-        const int nh = min(SEL_HEADS, G - h0);
-        __syncthreads();
-        for (int i = tid; i < SEL_HEADS * kD; i += THREADS) {
-            const int h = i / kD, d = i % kD;
-            sm.q[d & 31][d >> 5][h] = h < nh ? (double)key_to_float(static_cast<const TK*>(
-                                                   p.q)[((size_t)b * p.Hq + (size_t)kvh * G + h0 + h) * kD + d])
-                                             : 0.0;
-        }
-        __syncthreads();
-        // lane (r, c): block r of the 8, quarter c of its dims
-        const int r = lane >> 2, c = lane & 3;
-        int pages[SEL_AHEAD];
-        uint4 next[4];
-        auto means = [&](int page) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) next[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (page >= 0) {
-                const char* m = p.c.kmean + 2 * (((size_t)page * p.c.Hkv + kvh) * kD + 32 * c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const uint4*>(m + 16 * i);
-            }
-        };
-        for (int rb0 = r0 + warp * SEL_ROWS; rb0 < r1; rb0 += SEL_AHEAD * WARPS * SEL_ROWS) {
-#pragma unroll
-            for (int i = 0; i < SEL_AHEAD; ++i) {
-                const int row = rb0 + i * WARPS * SEL_ROWS + r;
-                pages[i] = row < r1 ? kv8_page(p.c, b, jlo + row) : -1;
-            }
-            means(pages[0]);
-#pragma unroll
-            for (int it = 0; it < SEL_AHEAD; ++it) {
-            const int rb = rb0 + it * WARPS * SEL_ROWS, row = rb + r, page = pages[it];
-            if (rb >= r1) break;
-            const uint4 w[4] = {next[0], next[1], next[2], next[3]};
-            if (it + 1 < SEL_AHEAD) means(pages[it + 1]);   // on their way while these are worked on
-            double acc[2][2] = {};   // two chains
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const double x = (double)key_to_float(reinterpret_cast<const TK*>(&w[e >> 3])[e & 7]);
-                mma_f64(acc[e & 1], x, sm.q[e][c][r]);
-            }
-            // this lane: the heads 2 c and 2 c + 1 of its block
-            double best = -INFINITY;
-            bool nan = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const double a = acc[0][i] + acc[1][i];
-                if (2 * c + i < nh) {
-                    nan |= isnan(a);
-                    best = a > best ? a : best;
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                const double x = __shfl_xor_sync(0xffffffffu, best, o);
-                best = x > best ? x : best;
-            }
-            nan = (__ballot_sync(0xffffffffu, nan) >> (4 * r) & 15u) != 0;
-            if (c == 0 && row < r1) {
-                if (h0 > 0) {
-                    nan |= isnan(score[row]);
-                    best = score[row] > best ? score[row] : best;
-                }
-                score[row] = page < 0 ? -INFINITY : nan ? NAN : best;
-            }
-            }
-        }
-    }
     if (cs > 1)
-        cluster.sync();   // the slice is scored, and the first CTA runs
+        cluster.sync();   // the first CTA runs, its shared memory is as above
     else
         __syncthreads();
-    u64* dst = cluster.map_shared_rank(key, 0);
-    for (int i = r0 + tid; i < r1; i += THREADS) {
-        const double x = score[i];
-        dst[i] = ordered(isnan(x) ? -INFINITY : x);
+    float* dst = cluster.map_shared_rank(score, 0);
+    SelSmem& first = *cluster.map_shared_rank(&sm, 0);
+    const int per = ((n + cs - 1) / cs + SEL_ROWS - 1) / SEL_ROWS * SEL_ROWS, r0 = min(n, rank * per), r1 = min(n, r0 + per);
+    uint32_t mean_max = 0;
+    for (int h0 = 0; h0 < G; h0 += SEL_ROWS / 2) {
+        const int nh = min(SEL_ROWS / 2, G - h0);
+        // the second operand: head r, dims 16 i + 4 c .. + 3
+        uint2 q[8];
+        float q1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            q[i] = make_uint2(0u, 0u);
+            if (r < nh)
+                q[i] = *reinterpret_cast<const uint2*>(static_cast<const TK*>(p.q) +
+                                                       ((size_t)b * p.Hq + (size_t)kvh * G + h0 + r) * kD + 16 * i + 4 * c);
+            const float2 x = KeyType<TK>::unpack(q[i].x), y = KeyType<TK>::unpack(q[i].y);
+            q1 += fabsf(x.x) + fabsf(x.y) + (fabsf(y.x) + fabsf(y.y));
+        }
+        q1 += __shfl_xor_sync(0xffffffffu, q1, 1);
+        q1 += __shfl_xor_sync(0xffffffffu, q1, 2);
+        if (rank == 0 && warp == 0 && c == 0) atomicMax(&sm.q1, __float_as_uint(q1));   // positive: bits order as values
+        for (int base = r0 + warp * SEL_ROWS; base < r1; base += SEL_AHEAD * WARPS * SEL_ROWS) {
+            int pages[SEL_AHEAD][2];
+#pragma unroll
+            for (int i = 0; i < SEL_AHEAD; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row = base + i * WARPS * SEL_ROWS + 8 * x + r;
+                    pages[i][x] = row < r1 ? kv8_page(p.c, b, jlo + row) : -1;
+                }
+#pragma unroll
+            for (int i = 0; i < SEL_AHEAD; ++i) {
+                const int rows = base + i * WARPS * SEL_ROWS;
+                if (rows >= r1) break;
+                uint2 w[2][8];
+                uint32_t big[2] = {0, 0};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const char* m = p.c.kmean + 2 * (((size_t)max(pages[i][x], 0) * p.c.Hkv + kvh) * kD + 4 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[x][e] = pages[i][x] >= 0 ? *reinterpret_cast<const uint2*>(m + 32 * e) : make_uint2(0u, 0u);
+                }
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    mma16816<KeyType<TK>::kBf>(d, w[0][e].x, w[1][e].x, w[0][e].y, w[1][e].y, q[e].x, q[e].y);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        big[x] = __vmaxu2(big[x], __vmaxu2(w[x][e].x & 0x7fff7fffu, w[x][e].y & 0x7fff7fffu));
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row = rows + 8 * x + r;
+                    // of the heads 2 c and 2 c + 1; a sum that is not finite makes the block's score NaN
+                    float s = -INFINITY;
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (2 * c + e < nh) {
+                            odd |= !isfinite(d[2 * x + e]);
+                            s = fmaxf(s, d[2 * x + e]);
+                        }
+                    s = quad_max(s);
+                    odd = (__ballot_sync(0xffffffffu, odd) >> (4 * r) & 15u) != 0;
+                    if (row < r1 && !odd) mean_max = max(mean_max, max(big[x] & 0xffffu, big[x] >> 16));
+                    if (c == 0 && row < r1) {
+                        if (h0 > 0) s = fmaxf(s, dst[row]);
+                        if (odd || (h0 > 0 && isnan(dst[row])) || pages[i][x] < 0) s = NAN;
+                        dst[row] = s;
+                    }
+                }
+            }
+        }
     }
+    mean_max = __reduce_max_sync(0xffffffffu, mean_max);
+    if (lane == 0) atomicMax(&first.mean_max, mean_max);
     if (cs > 1)
         cluster.sync();
     else
         __syncthreads();
     if (rank != 0) return;
 
-    // of the keys that compete, `need` are taken
+    // of the blocks that compete (the first n_first and last n_last are taken anyhow), `need` are taken
     int need = p.n_select - p.n_first - p.n_last;
-    const int rivals = n - p.n_first - p.n_last;
-    if (tid == 0) {
-        sm.thr = ~0ULL;
-        sm.need_eq = 0;
-        sm.n_list = 0;
-    }
-    __syncthreads();
-    if (need > 0 && rivals <= SEL_FEW) {
-        if (tid < rivals) sm.list[tid] = key[p.n_first + tid];
+    const int i0 = p.n_first, i1 = n - p.n_last;
+    bool exact = false;     // keys instead of scores
+    const bool some = need > 0;
+    if (some) {
+        float lo = INFINITY, hi = -INFINITY;
+        bool odd = false;
+        for (int i = i0 + tid; i < i1; i += THREADS) {
+            const float x = score[i];
+            odd |= isnan(x);
+            lo = fminf(lo, x);
+            hi = fmaxf(hi, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        float* wlo = reinterpret_cast<float*>(sm.lo);
+        float* whi = reinterpret_cast<float*>(sm.hi);
+        if (lane == 0) {
+            wlo[warp] = lo;
+            whi[warp] = hi;
+        }
+        exact = __syncthreads_or(odd);
+        if (!exact) {
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) {
+                lo = fminf(lo, wlo[i]);
+                hi = fmaxf(hi, whi[i]);
+            }
+            const float width = hi - lo, steps = width > 0.f ? (SEL_BINS - 1) / width : 0.f;
+            exact = !isfinite(width) || !isfinite(steps);   // the same for all threads
+            if (!exact) {
+                auto step = [&](float x) { return min(SEL_BINS - 1, (int)((x - lo) * steps)); };   // grows with x
+                for (int i = i0 + tid; i < i1; i += THREADS) atomicAdd(&sm.hist[step(score[i])], 1u);
+                __syncthreads();
+                find_step<THREADS>(sm, need);
+                const int bin = sm.bin;
+                for (int i = i0 + tid; i < i1; i += THREADS)
+                    if (step(score[i]) == bin) {
+                        atomicMin(&sm.v0, ordered(score[i]));
+                        atomicMax(&sm.v1, ordered(score[i]));
+                    }
+                __syncthreads();
+                const float eps = 0x1p-13f * __uint_as_float(sm.q1) * magnitude<TK>(sm.mean_max) + 0x1p-100f;
+                const float v0 = from_ordered(sm.v0) - 2.f * eps, v1 = from_ordered(sm.v1) + 2.f * eps;
+                // taken, not taken, and the list of those between
+                uint32_t above = 0;
+                for (int i = i0 + tid; i < i1; i += THREADS) {
+                    const float x = score[i];
+                    if (x > v1) {
+                        score[i] = INFINITY;
+                        ++above;
+                    } else if (x < v0) {
+                        score[i] = -INFINITY;
+                    } else {
+                        const uint32_t at = atomicAdd(&sm.n_list, 1u);
+                        if (at < SEL_LIST) sm.index[at] = (uint16_t)i;
+                    }
+                }
+                above = __reduce_add_sync(0xffffffffu, above);
+                if (lane == 0) atomicAdd(&sm.taken, above);
+                __syncthreads();
+                const int between = sm.n_list;
+                exact = between > SEL_LIST;
+                if (!exact) {
+                    need -= sm.taken;
+                    for (int i = warp; i < between; i += WARPS) {
+                        const u64 k = exact_key<TK>(p, b, kvh, jlo + sm.index[i]);
+                        if (lane == 0) sm.list[i] = k;
+                    }
+                    __syncthreads();
+                    if (tid < between) {
+                        const u64 k = sm.list[tid];
+                        const int at = sm.index[tid];
+                        int before = 0;
+                        for (int i = 0; i < between; ++i) before += sm.list[i] > k || (sm.list[i] == k && sm.index[i] < at);
+                        score[at] = before < need ? INFINITY : -INFINITY;
+                    }
+                }
+            }
+        }
         __syncthreads();
-        rank_list(sm, rivals, need);
-    } else if (need > 0) {
+    }
+    if (exact) {
+        for (int i = i0 + warp; i < i1; i += WARPS) {
+            const u64 k = exact_key<TK>(p, b, kvh, jlo + i);
+            if (lane == 0) key[i] = k;
+        }
+        if (tid == 0) sm.n_list = 0;
+        __syncthreads();
         u64 lo = ~0ULL, hi = 0;
-        for (int i = p.n_first + tid; i < n - p.n_last; i += THREADS) {
+        for (int i = i0 + tid; i < i1; i += THREADS) {
             lo = min(lo, key[i]);
             hi = max(hi, key[i]);
         }
@@ -255,28 +400,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         u64 range = hi - lo;      // of the step looked at: keys lo .. lo + range
         for (;;) {
             const int shift = max(0, 64 - SEL_BITS - __clzll((long long)range));
-            for (int i = p.n_first + tid; i < n - p.n_last; i += THREADS)
+            for (int i = i0 + tid; i < i1; i += THREADS)
                 if (key[i] - lo <= range) atomicAdd(&sm.hist[(key[i] - lo) >> shift], 1u);
             __syncthreads();
-            // bins from the highest: thread i takes the next PER of them
-            constexpr int PER = SEL_BINS / THREADS;
-            uint32_t c[PER], mine = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                c[i] = sm.hist[SEL_BINS - 1 - (tid * PER + i)];
-                mine += c[i];
-            }
-            uint32_t before = cta_scan<WARPS>(mine, sm.red);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (before < (uint32_t)need && before + c[i] >= (uint32_t)need) {
-                    sm.bin = SEL_BINS - 1 - (tid * PER + i);
-                    sm.above = before;
-                    sm.count = c[i];
-                }
-                before += c[i];
-            }
-            __syncthreads();
+            find_step<THREADS>(sm, need);
             need -= sm.above;
             lo += (u64)sm.bin << shift;
             range = (1ULL << shift) - 1;
@@ -290,25 +417,34 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
                 break;
             }
             if (count <= SEL_LIST) {
-                for (int i = p.n_first + tid; i < n - p.n_last; i += THREADS)
+                for (int i = i0 + tid; i < i1; i += THREADS)
                     if (key[i] - lo <= range) sm.list[atomicAdd(&sm.n_list, 1u)] = key[i];
                 __syncthreads();
                 rank_list(sm, count, need);
                 break;
             }
-            for (int i = tid; i < SEL_BINS; i += THREADS) sm.hist[i] = 0;
-            __syncthreads();
+            __syncthreads();   // the step has been read
         }
     }
+    __syncthreads();
     // in order: a warp takes a run of candidates, 32 at a time; first how many before each warp's
     const u64 thr = sm.thr;
     const uint32_t need_eq = sm.need_eq;
-    const int run = ((n + WARPS - 1) / WARPS + 31) & ~31, i0 = min(n, warp * run), i1 = min(n, i0 + run);
+    auto taken = [&](int i, bool& same) {
+        same = false;
+        if (i >= n) return false;
+        if (i < i0 || i >= i1) return true;
+        if (!exact) return some && score[i] == INFINITY;
+        same = key[i] == thr;
+        return key[i] > thr;
+    };
+    const int run = ((n + WARPS - 1) / WARPS + 31) & ~31, w0 = min(n, warp * run), w1 = min(n, w0 + run);
     uint32_t gt = 0, eq = 0;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-        const bool in = i < i1, f = in && forced(p, i, n);
-        gt += __popc(__ballot_sync(0xffffffffu, f || (in && key[i] > thr)));
-        eq += __popc(__ballot_sync(0xffffffffu, in && !f && key[i] == thr));
+    bool same;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        const bool t = taken(i < w1 ? i : n, same);
+        gt += __popc(__ballot_sync(0xffffffffu, t));
+        eq += __popc(__ballot_sync(0xffffffffu, same));
     }
     if (lane == 0) sm.red[warp] = gt << 16 | eq;   // at most 16384 of each
     __syncthreads();
@@ -318,12 +454,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         if (i < warp) before += sm.red[i];
     uint32_t at = (before >> 16) + min(before & 0xffffu, need_eq), seen = before & 0xffffu;
     const uint32_t below = (1u << lane) - 1;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-        const bool in = i < i1, f = in && forced(p, i, n), same = in && !f && key[i] == thr;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        bool t = taken(i < w1 ? i : n, same);
         const uint32_t all_same = __ballot_sync(0xffffffffu, same);
-        const bool take = f || (in && key[i] > thr) || (same && seen + __popc(all_same & below) < need_eq);
-        const uint32_t all = __ballot_sync(0xffffffffu, take);
-        if (take) out[at + __popc(all & below)] = jlo + i;
+        t |= same && seen + __popc(all_same & below) < need_eq;
+        const uint32_t all = __ballot_sync(0xffffffffu, t);
+        if (t) out[at + __popc(all & below)] = jlo + i;
         at += __popc(all);
         seen += __popc(all_same);
     }
