@@ -29,7 +29,6 @@ namespace zgcm {
 namespace {
 
 constexpr int SEL_ROWS = 16;                      // blocks of a warp at a time
-constexpr int SEL_AHEAD = 2;                      // steps of a warp whose page numbers are looked up together
 constexpr int SEL_BITS = 10, SEL_BINS = 1 << SEL_BITS;
 constexpr int SEL_LIST = 256;                     // most keys ranked by counting
 
@@ -222,56 +221,52 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         q1 += __shfl_xor_sync(0xffffffffu, q1, 1);
         q1 += __shfl_xor_sync(0xffffffffu, q1, 2);
         if (rank == 0 && warp == 0 && c == 0) atomicMax(&sm.q1, __float_as_uint(q1));   // positive: bits order as values
-        for (int base = r0 + warp * SEL_ROWS; base < r1; base += SEL_AHEAD * WARPS * SEL_ROWS) {
-            int pages[SEL_AHEAD][2];
+        int pages[2];
+        auto look_up = [&](int rows) {
 #pragma unroll
-            for (int i = 0; i < SEL_AHEAD; ++i)
+            for (int x = 0; x < 2; ++x)
+                pages[x] = rows + 8 * x + r < r1 ? kv8_page(p.c, b, jlo + rows + 8 * x + r) : -1;
+        };
+        look_up(r0 + warp * SEL_ROWS);
+        for (int rows = r0 + warp * SEL_ROWS; rows < r1; rows += WARPS * SEL_ROWS) {
+            uint2 w[2][8];
+            uint32_t big[2] = {0, 0};
+            const bool bad[2] = {pages[0] < 0, pages[1] < 0};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int row = base + i * WARPS * SEL_ROWS + 8 * x + r;
-                    pages[i][x] = row < r1 ? kv8_page(p.c, b, jlo + row) : -1;
-                }
+            for (int x = 0; x < 2; ++x) {
+                const char* m = p.c.kmean + 2 * (((size_t)max(pages[x], 0) * p.c.Hkv + kvh) * kD + 4 * c);
 #pragma unroll
-            for (int i = 0; i < SEL_AHEAD; ++i) {
-                const int rows = base + i * WARPS * SEL_ROWS;
-                if (rows >= r1) break;
-                uint2 w[2][8];
-                uint32_t big[2] = {0, 0};
+                for (int e = 0; e < 8; ++e)
+                    w[x][e] = bad[x] ? make_uint2(0u, 0u) : *reinterpret_cast<const uint2*>(m + 32 * e);
+            }
+            look_up(rows + WARPS * SEL_ROWS);   // the next step's, while the means come
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const char* m = p.c.kmean + 2 * (((size_t)max(pages[i][x], 0) * p.c.Hkv + kvh) * kD + 4 * c);
+            for (int e = 0; e < 8; ++e) {
+                mma16816<KeyType<TK>::kBf>(d, w[0][e].x, w[1][e].x, w[0][e].y, w[1][e].y, q[e].x, q[e].y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[x][e] = pages[i][x] >= 0 ? *reinterpret_cast<const uint2*>(m + 32 * e) : make_uint2(0u, 0u);
-                }
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int x = 0; x < 2; ++x)
+                    big[x] = __vmaxu2(big[x], __vmaxu2(w[x][e].x & 0x7fff7fffu, w[x][e].y & 0x7fff7fffu));
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    mma16816<KeyType<TK>::kBf>(d, w[0][e].x, w[1][e].x, w[0][e].y, w[1][e].y, q[e].x, q[e].y);
+            for (int x = 0; x < 2; ++x) {
+                const int row = rows + 8 * x + r;
+                // of the heads 2 c and 2 c + 1; a sum that is not finite makes the block's score NaN
+                float s = -INFINITY;
+                bool odd = false;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        big[x] = __vmaxu2(big[x], __vmaxu2(w[x][e].x & 0x7fff7fffu, w[x][e].y & 0x7fff7fffu));
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int row = rows + 8 * x + r;
-                    // of the heads 2 c and 2 c + 1; a sum that is not finite makes the block's score NaN
-                    float s = -INFINITY;
-                    bool odd = false;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (2 * c + e < nh) {
-                            odd |= !isfinite(d[2 * x + e]);
-                            s = fmaxf(s, d[2 * x + e]);
-                        }
-                    s = quad_max(s);
-                    odd = (__ballot_sync(0xffffffffu, odd) >> (4 * r) & 15u) != 0;
-                    if (row < r1 && !odd) mean_max = max(mean_max, max(big[x] & 0xffffu, big[x] >> 16));
-                    if (c == 0 && row < r1) {
-                        if (h0 > 0) s = fmaxf(s, dst[row]);
-                        if (odd || (h0 > 0 && isnan(dst[row])) || pages[i][x] < 0) s = NAN;
-                        dst[row] = s;
+                for (int e = 0; e < 2; ++e)
+                    if (2 * c + e < nh) {
+                        odd |= !isfinite(d[2 * x + e]);
+                        s = fmaxf(s, d[2 * x + e]);
                     }
+                s = quad_max(s);
+                odd = (__ballot_sync(0xffffffffu, odd) >> (4 * r) & 15u) != 0;
+                if (row < r1 && !odd) mean_max = max(mean_max, max(big[x] & 0xffffu, big[x] >> 16));
+                if (c == 0 && row < r1) {
+                    if (h0 > 0) s = fmaxf(s, dst[row]);
+                    if (odd || (h0 > 0 && isnan(dst[row])) || bad[x]) s = NAN;
+                    dst[row] = s;
                 }
             }
         }
@@ -427,41 +422,36 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         }
     }
     __syncthreads();
-    // in order: a warp takes a run of candidates, 32 at a time; first how many before each warp's
+    // In order: a warp takes a run of candidates, at most 32 x 32, lane i the 32 from 32 i: which of them are taken, and
+    // which are equal to the threshold; then where each lane's go.
     const u64 thr = sm.thr;
-    const uint32_t need_eq = sm.need_eq;
-    auto taken = [&](int i, bool& same) {
-        same = false;
-        if (i >= n) return false;
-        if (i < i0 || i >= i1) return true;
-        if (!exact) return some && score[i] == INFINITY;
-        same = key[i] == thr;
-        return key[i] > thr;
-    };
-    const int run = ((n + WARPS - 1) / WARPS + 31) & ~31, w0 = min(n, warp * run), w1 = min(n, w0 + run);
-    uint32_t gt = 0, eq = 0;
-    bool same;
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-        const bool t = taken(i < w1 ? i : n, same);
-        gt += __popc(__ballot_sync(0xffffffffu, t));
-        eq += __popc(__ballot_sync(0xffffffffu, same));
+    const int need_eq = sm.need_eq;
+    const int run = ((n + WARPS - 1) / WARPS + 31) & ~31, w0 = warp * run;
+    static_assert(kKv8MaxBlocks <= 1024 * 16, "a lane for each 32 of a warp's run");
+    uint32_t mine = 0, mine_eq = 0;
+    for (int it = 0; it * 32 < run; ++it) {
+        const int i = w0 + it * 32 + lane;
+        bool t = i < n, same = false;
+        if (t && i >= i0 && i < i1) {
+            if (exact) {
+                t = key[i] > thr;
+                same = key[i] == thr;
+            } else {
+                t = some && score[i] == INFINITY;
+            }
+        }
+        const uint32_t all = __ballot_sync(0xffffffffu, t), all_same = __ballot_sync(0xffffffffu, same);
+        if (it == lane) {
+            mine = all;
+            mine_eq = all_same;
+        }
     }
-    if (lane == 0) sm.red[warp] = gt << 16 | eq;   // at most 16384 of each
-    __syncthreads();
-    uint32_t before = 0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i)
-        if (i < warp) before += sm.red[i];
-    uint32_t at = (before >> 16) + min(before & 0xffffu, need_eq), seen = before & 0xffffu;
-    const uint32_t below = (1u << lane) - 1;
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-        bool t = taken(i < w1 ? i : n, same);
-        const uint32_t all_same = __ballot_sync(0xffffffffu, same);
-        t |= same && seen + __popc(all_same & below) < need_eq;
-        const uint32_t all = __ballot_sync(0xffffffffu, t);
-        if (t) out[at + __popc(all & below)] = jlo + i;
-        at += __popc(all);
-        seen += __popc(all_same);
+    const uint32_t before = cta_scan<WARPS>(__popc(mine) << 16 | __popc(mine_eq), sm.red);   // at most 16384 of each
+    int seen = before & 0xffffu, at = (before >> 16) + min(seen, need_eq);
+    for (uint32_t left = mine | mine_eq; left; left &= left - 1) {
+        const uint32_t bit = left & -left;
+        if ((mine & bit) || seen < need_eq) out[at++] = jlo + w0 + 32 * lane + __ffs(bit) - 1;
+        seen += (mine_eq & bit) != 0;
     }
 }
 
