@@ -671,91 +671,32 @@ def zgcm_proj_out_bwd(a, w_o, dy, *, da=None, dw=None, stream=None):
 
 # ------------------------------------- q/k normalisation and rotation (zgcm_qkrope.h)
 #
-# These calls and those of zgcm_kv8.h run in decode steps of a few microseconds, so their checks
-# look at each tensor once and pass plain integers to ctypes.
+# The calls of a decode step check their tensors in csrc/torch_calls.cpp (the module _calls), by the
+# same rules: from Python that took several times as long as their kernels.  `stream`: a torch stream of the
+# tensors' device (default: its current one); outputs and workspaces that are not given belong to it.
 
-_NORM_TYPES = {}   # torch dtype -> zgcm_dtype
-
-
-def _type_code(t, name):
-    import torch
-    if not _NORM_TYPES:
-        _NORM_TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    code = _NORM_TYPES.get(t)
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32")
-    return code
+_module = None
 
 
-def _is(t, name, dtype, shape, index):
-    """t: a contiguous tensor of `dtype` and exactly `shape` on CUDA device `index`; its address."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
-                        f"{tuple(t.shape)}")
-    if t.get_device() != index:
-        raise _device_error(name, t, index)
-    return t.data_ptr()
+def _quick():
+    global _module
+    if _module is None:
+        load()
+        import torch  # noqa: F401  (the module's libraries)
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(HERE, '_calls.so')} cannot be loaded ({e}): build it with "
+                               "`python -m global_attention_b200.build` (no CPU fallback exists)") from e
+        _module = _calls
+    return _module
 
 
-def _device_error(name, t, index):
-    if not t.is_cuda:
-        return TypeError(f"{name} must be a CUDA tensor")
-    return TypeError(f"{name} must be on the device of the other tensors (cuda:{index})")
-
-
-def _rows(t, name, dtype, shape, index, out=False):
-    """t: a [T, H, D] tensor of `dtype` on CUDA device `index` whose rows of D are contiguous; its zgcm_rows.  The
-    stride of a dimension of one is not looked at (torch lets it be anything).  out: no two elements in one place."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype or t.shape != shape:
-        raise TypeError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise _device_error(name, t, index)
-    T, H, D = shape
-    ts, hs, ds = t.stride()
-    if ds != 1 and D > 1:
-        raise TypeError(f"{name} must have contiguous rows")
-    if T <= 1:
-        ts = 0
-    if H <= 1:
-        hs = 0
-    if out and T > 0:
-        reach = D
-        for s, n in sorted(((ts, T), (hs, H))):
-            if n > 1:
-                if s < reach:
-                    raise TypeError(f"{name} must not overlap itself")
-                reach += s * (n - 1)
-    return _Rows(t.data_ptr(), ts, hs)
-
-
-def _run(index, stream, fn, *args):
-    """fn(*args, stream) with device `index` current; stream: a torch stream or None (the device's current one)."""
-    import torch
-    if torch._C._cuda_getDevice() != index:
-        with torch.cuda.device(index):
-            return _run(index, stream, fn, *args)
-    return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-
-
-def _qk_check(q, k, gamma_q, gamma_k, pos):
-    import torch
-    for n, t in (("q", q), ("k", k)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise TypeError(f"{n} must be a tensor of rank 3")
-    T, Hq, D = q.shape
-    Hkv, dtype, index = k.shape[1], q.dtype, q.get_device()
-    code = _type_code(dtype, "q")
-    rq, rk = _rows(q, "q", dtype, (T, Hq, D), index), _rows(k, "k", dtype, (T, Hkv, D), index)
-    f32 = torch.float32
-    pg = _is(gamma_q, "gamma_q", f32, (D,), index), _is(gamma_k, "gamma_k", f32, (D,), index)
-    pp = _is(pos, "pos", torch.int32, (T,), index)
-    return T, Hq, Hkv, D, code, index, rq, rk, *pg, pp
+def _done(result, what):
+    if result.__class__ is int:   # a status
+        if result != ZGCM_OK:
+            raise ZgcmError(result, what)
+    return result
 
 
 def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_base=10000.0, eps=1e-6, out_dtype=None,
@@ -763,27 +704,8 @@ def zgcm_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, *, rope_dims=42, rope_bas
     """RMSNorm of every head's row, times gamma, rotated at the token's position: q [T,Hq,D], k [T,Hkv,D]
     (bf16, fp16 or fp32, rows contiguous, any token and head strides that are multiples of 8), pos int32
     [T].  Returns (qr, kr) of out_dtype (default: q's), or writes the tensors given."""
-    import torch
-    T, Hq, Hkv, D, xt, index, rq, rk, pgq, pgk, pp = _qk_check(q, k, gamma_q, gamma_k, pos)
-    if out_dtype is None:
-        given = qr if qr is not None else kr
-        out_dtype = q.dtype if given is None else given.dtype
-    yt = _type_code(out_dtype, "out_dtype")
-    rqr = None if qr is None else _rows(qr, "qr", out_dtype, (T, Hq, D), index, out=True)
-    rkr = None if kr is None else _rows(kr, "kr", out_dtype, (T, Hkv, D), index, out=True)
-    if index < 0:
-        raise TypeError("q must be a CUDA tensor")
-    if qr is None:
-        qr = q.new_empty((T, Hq, D), dtype=out_dtype)
-        rqr = _Rows(qr.data_ptr(), Hq * D, D)
-    if kr is None:
-        kr = q.new_empty((T, Hkv, D), dtype=out_dtype)
-        rkr = _Rows(kr.data_ptr(), Hkv * D, D)
-    st = _run(index, stream, load().zgcm_qk_norm_rope_fwd, rq, rk, pgq, pgk, pp, T, Hq, Hkv, D, xt, yt, int(rope_dims),
-              float(rope_base), float(eps), rqr, rkr)
-    if st != ZGCM_OK:
-        raise ZgcmError(st, "zgcm_qk_norm_rope_fwd")
-    return qr, kr
+    return _done(_quick().qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, rope_dims, rope_base, eps, out_dtype, qr, kr, stream),
+                 "zgcm_qk_norm_rope_fwd")
 
 
 def zgcm_qk_norm_rope_bwd_workspace_size(T) -> int:
@@ -795,45 +717,14 @@ def zgcm_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, dqr, dkr, *, rope_dims=42
                           grads=None, workspace=None, stream=None):
     """Gradients of zgcm_qk_norm_rope_fwd: dict dq, dk (q's dtype), dgamma_q, dgamma_k (fp32 [D], overwritten).
     `grads` may supply them, `workspace` a uint8 tensor of zgcm_qk_norm_rope_bwd_workspace_size(T) bytes."""
-    import torch
-    T, Hq, Hkv, D, xt, index, rq, rk, pgq, pgk, pp = _qk_check(q, k, gamma_q, gamma_k, pos)
-    if not isinstance(dqr, torch.Tensor):
-        raise TypeError("dqr must be a torch tensor")
-    yt = _type_code(dqr.dtype, "dqr")
-    rdqr = _rows(dqr, "dqr", dqr.dtype, (T, Hq, D), index)
-    rdkr = _rows(dkr, "dkr", dqr.dtype, (T, Hkv, D), index)
-    if workspace is not None:
-        _is(workspace, "workspace", torch.uint8, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else (), index)
-    if grads is not None:
-        rdq = _rows(grads["dq"], "dq", q.dtype, (T, Hq, D), index, out=True)
-        rdk = _rows(grads["dk"], "dk", q.dtype, (T, Hkv, D), index, out=True)
-        pdgq = _is(grads["dgamma_q"], "dgamma_q", torch.float32, (D,), index)
-        pdgk = _is(grads["dgamma_k"], "dgamma_k", torch.float32, (D,), index)
-    if index < 0:
-        raise TypeError("q must be a CUDA tensor")
-    if grads is None:
-        dq, dk = q.new_empty((T, Hq, D)), k.new_empty((T, Hkv, D))
-        dgq, dgk = gamma_q.new_empty(D), gamma_k.new_empty(D)
-        rdq, rdk = _Rows(dq.data_ptr(), Hq * D, D), _Rows(dk.data_ptr(), Hkv * D, D)
-        pdgq, pdgk = dgq.data_ptr(), dgk.data_ptr()
-        grads = {"dq": dq, "dk": dk, "dgamma_q": dgq, "dgamma_k": dgk}
-    lib = load()
-    if workspace is None:
-        workspace = gamma_q.new_empty(max(4, lib.zgcm_qk_norm_rope_bwd_workspace_size(T) // 4))
-    st = _run(index, stream, lib.zgcm_qk_norm_rope_bwd, rq, rk, pgq, pgk, pp, rdqr, rdkr, T, Hq, Hkv, D, xt, yt,
-              int(rope_dims), float(rope_base), float(eps), rdq, rdk, pdgq, pdgk, workspace.data_ptr(), workspace.nbytes)
-    if st != ZGCM_OK:
-        raise ZgcmError(st, "zgcm_qk_norm_rope_bwd")
-    return grads
+    g = (None,) * 4 if grads is None else (grads["dq"], grads["dk"], grads["dgamma_q"], grads["dgamma_k"])
+    return _done(_quick().qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, dqr, dkr, rope_dims, rope_base, eps, *g, workspace, stream),
+                 "zgcm_qk_norm_rope_bwd")
 
 
 # ------------------------------------------------- 8-bit block cache (zgcm_kv8.h)
 
 KV8_BLOCK = 64
-
-
-def _window(w):
-    return min(int(w), 2 ** 31 - 1)   # a C int: any window this long reaches everything
 
 
 class ZgcmKv8Cache:
@@ -869,10 +760,10 @@ class ZgcmKv8Cache:
         _one_device(*zip(self._NAMES, tensors))
         self._t = dict(zip(self._NAMES, tensors))
         self.n_seq, self.n_blocks, self.n_pages, self.Hkv, self.D = n_seq, n_blocks, P, Hkv, D
-        self.key_dtype, self.device, self._index = k_tail.dtype, k_codes.device, k_codes.get_device()
+        self.key_dtype, self.device = k_tail.dtype, k_codes.device
         self._c = _Kv8Struct(*(t.data_ptr() for t in tensors), n_seq, n_blocks, P, Hkv, D,
                              0 if k_codes.dtype == torch.float8_e4m3fn else 1, 0 if k_tail.dtype == torch.bfloat16 else 1)
-        self._ref = ctypes.byref(self._c)
+        self._handle = ctypes.addressof(self._c), k_codes
 
     def __getattr__(self, name):
         t = self.__dict__.get("_t", {})
@@ -909,59 +800,24 @@ def zgcm_kv8_alloc(n_seq, n_blocks, Hkv, *, n_pages=None, D=128, code_dtype=None
                         torch.zeros(tails, dtype=torch.bfloat16, device=device), table)
 
 
-def _kv8_cache(cache):
+def _kv8(cache):
     if not isinstance(cache, ZgcmKv8Cache):
         raise TypeError("cache must be a ZgcmKv8Cache")
-    return cache._index
-
-
-def _kv8_query(cache, q):
-    """Query heads of q [n_seq, Hq, D]."""
-    import torch
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a tensor of rank 3")
-    return q.shape[1]
-
-
-def _kv8_tokens(cache, t, name, dtype, N, index):
-    """Address and strides of k or v [n_seq, N, Hkv, D] with contiguous rows."""
-    import torch
-    shape = (cache.n_seq, N, cache.Hkv, cache.D)
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
-        raise TypeError(f"{name} must be a {dtype} tensor of shape {shape}")
-    if t.get_device() != index:
-        raise _device_error(name, t, index)
-    b, n, h, d = t.stride()
-    if d != 1 and cache.D > 1:
-        raise TypeError(f"{name} must have contiguous rows")
-    return t.data_ptr(), b if shape[0] > 1 else 0, n if N > 1 else 0, h if shape[2] > 1 else 0
+    return cache._handle
 
 
 def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
     """Append tokens: k (cache.key_dtype, prepared: zgcm_qk_norm_rope_fwd) and v (bf16) [n_seq, N, Hkv, D], rows
     contiguous, other strides multiples of 8; pos int32 [n_seq], the first token's position (negative: the sequence
     is idle); count int32 [n_seq], the tokens of each sequence (default N).  Updates the cache in place."""
-    import torch
-    index = _kv8_cache(cache)
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise TypeError("k must be a tensor of rank 4")
-    N = k.shape[1]
-    pk = _kv8_tokens(cache, k, "k", cache.key_dtype, N, index)
-    pv = _kv8_tokens(cache, v, "v", torch.bfloat16, N, index)
-    pp = _is(pos, "pos", torch.int32, (cache.n_seq,), index)
-    pc = None if count is None else _is(count, "count", torch.int32, (cache.n_seq,), index)
-    if index < 0:
-        raise TypeError("k must be a CUDA tensor")
-    st = _run(index, stream, load().zgcm_kv8_append, cache._ref, *pk, *pv, pp, pc, N)
-    if st != ZGCM_OK:
-        raise ZgcmError(st, "zgcm_kv8_append")
+    _done(_quick().kv8_append(*_kv8(cache), k, v, pos, count, stream), "zgcm_kv8_append")
     return cache
 
 
 def zgcm_attn_decode_kv8_workspace_size(cache, Hq, *, window=128, n_list=None) -> int:
     """Bytes of workspace zgcm_attn_decode_kv8 needs (n_list: the last dimension of `blocks`, if given)."""
-    _kv8_cache(cache)
-    return int(load().zgcm_attn_decode_kv8_workspace_size(cache._ref, int(Hq), _window(window),
+    _kv8(cache)
+    return int(load().zgcm_attn_decode_kv8_workspace_size(ctypes.byref(cache._c), int(Hq), min(int(window), 2 ** 31 - 1),
                                                           -1 if n_list is None else int(n_list)))
 
 
@@ -969,70 +825,15 @@ def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=Non
                          stream=None):
     """Decode attention of one token per sequence, the newest one appended: q [n_seq,Hq,D] (cache.key_dtype, prepared),
     g bf16 [n_seq,Hq,D] or None (no gate), pos int32 [n_seq].  blocks: int32 [n_seq,Hkv,n] from zgcm_kv8_select, the
-    earlier blocks to read (default: all that the window reaches).  Returns (out bf16 [n_seq,Hq,D], lse fp32 [n_seq,Hq])."""
-    import torch
-    index = _kv8_cache(cache)
-    Hq = _kv8_query(cache, q)
-    B, D = cache.n_seq, cache.D
-    shape = (B, Hq, D)
-    pq = _is(q, "q", cache.key_dtype, shape, index)
-    pg = None if g is None else _is(g, "g", torch.bfloat16, shape, index)
-    pp = _is(pos, "pos", torch.int32, (B,), index)
-    pb, n_list = None, 0
-    if blocks is not None:
-        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3:
-            raise TypeError("blocks must be a tensor of rank 3")
-        n_list = blocks.shape[2]
-        pb = _is(blocks, "blocks", torch.int32, (B, cache.Hkv, n_list), index)
-        if n_list == 0:
-            pb = pp   # an empty list is not read: only that there is one counts
-    if out is not None:
-        _is(out, "out", torch.bfloat16, shape, index)
-    if lse is not None:
-        _is(lse, "lse", torch.float32, (B, Hq), index)
-    if workspace is not None:
-        _is(workspace, "workspace", torch.uint8, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else (), index)
-    if index < 0:
-        raise TypeError("q must be a CUDA tensor")
-    if out is None:
-        out = cache._t["v_tail"].new_empty(shape)
-    lib, window, fp32 = load(), _window(window), cache._t["k_scale"]
-    if lse is None:
-        lse = fp32.new_empty((B, Hq))
-    pw, nw = None, 0
-    if workspace is None:
-        nw = lib.zgcm_attn_decode_kv8_workspace_size(cache._ref, Hq, window, -1 if blocks is None else n_list)
-        if nw:
-            workspace = fp32.new_empty(nw // 4)
-            pw = workspace.data_ptr()
-    else:
-        pw, nw = workspace.data_ptr(), workspace.numel()
-    st = _run(index, stream, lib.zgcm_attn_decode_kv8, cache._ref, pq, pg, pp, pb, n_list, Hq, window,
-              1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), pw, nw)
-    if st != ZGCM_OK:
-        raise ZgcmError(st, "zgcm_attn_decode_kv8")
-    return out, lse
+    earlier blocks to read (default: all that the window reaches).  workspace: a uint8 tensor of
+    zgcm_attn_decode_kv8_workspace_size bytes.  Returns (out bf16 [n_seq,Hq,D], lse fp32 [n_seq,Hq])."""
+    handle = _kv8(cache)
+    return _done(_quick().attn_decode_kv8(*handle, q, g, pos, blocks, window, cache.D ** -0.5 if scale is None else scale, out,
+                                          lse, workspace, stream), "zgcm_attn_decode_kv8")
 
 
 def zgcm_kv8_select(cache, q, pos, n_select, *, n_first=1, n_last=1, window=128, out=None, stream=None):
     """The blocks a decode step should read: int32 [n_seq, Hkv, n_select], ascending, -1 behind the last, for
     zgcm_attn_decode_kv8(blocks=...).  q [n_seq,Hq,D] (cache.key_dtype, prepared); a block's score is the largest
     q . (mean of its keys) over the KV head's queries; the first n_first and last n_last candidates always count."""
-    import torch
-    index = _kv8_cache(cache)
-    Hq, n_select = _kv8_query(cache, q), int(n_select)
-    B = cache.n_seq
-    pq = _is(q, "q", cache.key_dtype, (B, Hq, cache.D), index)
-    pp = _is(pos, "pos", torch.int32, (B,), index)
-    shape = (B, cache.Hkv, max(0, n_select))
-    if out is not None:
-        _is(out, "out", torch.int32, shape, index)
-    if index < 0:
-        raise TypeError("q must be a CUDA tensor")
-    if out is None:
-        out = cache._t["table"].new_empty(shape)
-    st = _run(index, stream, load().zgcm_kv8_select, cache._ref, pq, pp, Hq, _window(window), n_select, int(n_first),
-              int(n_last), out.data_ptr())
-    if st != ZGCM_OK:
-        raise ZgcmError(st, "zgcm_kv8_select")
-    return out
+    return _done(_quick().kv8_select(*_kv8(cache), q, pos, n_select, n_first, n_last, window, out, stream), "zgcm_kv8_select")

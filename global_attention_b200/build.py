@@ -3,7 +3,8 @@
     python -m global_attention_b200.build [--verbose]
 
 Each csrc/*.cu is compiled by nvcc for sm_100a (objects under _build/), then linked into
-one shared library with the CUDA runtime linked statically.
+one shared library with the CUDA runtime linked statically.  csrc/torch_calls.cpp, the binding's
+quick calls, becomes the extension module global_attention_b200/_calls.so against it and torch.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libzgcm_attn.so")
+CALLS = os.path.join(HERE, "_calls.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -58,7 +62,28 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    build_calls(force)
     return LIB
+
+
+def build_calls(force: bool = False) -> str:
+    """The extension module of csrc/torch_calls.cpp (host code; the library beside it is found by $ORIGIN)."""
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    if force or _needs(CALLS, [src, __file__, *glob.glob(os.path.join(ROOT, "include", "*.h"))]):
+        import torch
+        base = os.path.dirname(torch.__file__)
+        inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
+        cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *("-I" + d for d in inc),
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", CALLS + ".tmp",
+               "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ltorch",
+               "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{CXX} failed on {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":

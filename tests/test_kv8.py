@@ -14,6 +14,7 @@ times its largest |v|.  The output is rounded once to bf16 (2^-8 of the value). 
 Selected blocks: equal.
 """
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -691,6 +692,63 @@ def test_graphs_follow_positions(cuda):
                     ref = kv8.attend(q[b], g[b], k[b, :p + 1], v[b, :p + 1], code="e4m3", window=100 if windowed else ALL,
                                      blocks=None if bl is None else bl[b].cpu().numpy())
                     _close((p, b), out[b], lse[b], *ref, q[b], k[b, :p + 1], 128 ** -0.5)
+
+
+def _one_history(B, S, seed):
+    """A cache of B sequences whose tables name the same pages: one history of S tokens, read by all."""
+    k, v = _tokens(1, S, 1, "bf16", seed=seed)
+    c = _new(B, S // 64 + 1, 1, "e4m3", "bf16", seed=seed)
+    ga.zgcm_kv8_append(c, k.cuda().expand(B, -1, -1, -1), v.cuda().expand(B, -1, -1, -1), _i32(0, *[-1] * (B - 1)))
+    c.table.copy_(c.table[:1].clone().expand(B, -1))
+    c.k_tail.copy_(c.k_tail[:1].clone().expand(B, -1, -1, -1))
+    c.v_tail.copy_(c.v_tail[:1].clone().expand(B, -1, -1, -1))
+    return c, k[0], v[0]
+
+
+@gpu
+def test_graphs_share_a_records_workspace(cuda):
+    """Enough long sequences that the work is split over a workspace of records: two graphs that hold the same
+    one, replayed in turn, and calls on a stream of their own with a workspace that nobody keeps."""
+    B, S = 150, 4300
+    histories = [_one_history(B, S, seed) for seed in (21, 22)]
+    q, g = _queries(B, 8, "bf16")
+    qd, gd, pos = q.cuda(), g.cuda(), _i32(*[S - 1] * B)
+    need = ga.zgcm_attn_decode_kv8_workspace_size(histories[0][0], 8, window=ALL)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    alone = [ga.zgcm_attn_decode_kv8(c, qd, gd, pos, window=ALL, workspace=ws) for c, _, _ in histories]
+    for (out, lse), (c, k, v) in zip(alone, histories):
+        for b in (0, 77, B - 1):
+            ref = kv8.attend(q[b], g[b], k, v, code="e4m3", window=ALL)
+            _close(b, out[b], lse[b], *ref, q[b], k, 128 ** -0.5)
+    graphs, got = [], []
+    for c, _, _ in histories:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(ga.zgcm_attn_decode_kv8(c, qd, gd, pos, window=ALL, workspace=ws))
+        graphs.append(graph)
+    for _ in range(5):
+        for x in got:
+            x[0].zero_()
+        for graph in graphs:
+            graph.replay()
+        for x, y in zip(got, alone):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kept = []
+    for i in range(10):
+        kept.append(ga.zgcm_attn_decode_kv8(histories[i % 2][0], qd, gd, pos, window=ALL, stream=side))
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)   # on the current stream, meanwhile
+    torch.cuda.synchronize()
+    for i, x in enumerate(kept):
+        assert torch.equal(x[0], alone[i % 2][0]) and torch.equal(x[1], alone[i % 2][1])
+    other = types.SimpleNamespace(device_index=1 + torch.cuda.current_device(), cuda_stream=0)
+    for call in (lambda: ga.zgcm_attn_decode_kv8(histories[0][0], qd, gd, pos, window=ALL, stream=other),
+                 lambda: ga.zgcm_kv8_select(histories[0][0], qd, pos, 4, stream=other)):
+        with pytest.raises(TypeError, match="stream"):
+            call()
+    assert ga.zgcm_attn_device_error() == 0
 
 
 @gpu
