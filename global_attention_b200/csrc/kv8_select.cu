@@ -7,8 +7,8 @@
 // One pass over the block means, 256 bytes each.  The choice is that of fp64 sums (products of 16-bit values
 // are exact there and the sum of 128 of them is off by 2^-46 of its terms at most), but only blocks at the border
 // need them: the tensor cores give every score in fp32 (16 blocks by 8 heads an instruction), off by less than
-//      eps = 2^-13 max_h |q_h|_1 max_j |k_mean_j|_max
-// (8 sums of 17 terms, each off by 2^-22 of the largest of them at most: 2^-14.9 of the terms' sum); one histogram of 1024
+//      eps = 2^-14.5 max_h |q_h|_1 max_j |k_mean_j|_max
+// (8 sums of 17 terms, each off by 2^-22 of the largest of them at most: 2^-14.9 of the terms' sum; the histogram's own roundings are small against the rest); one histogram of 1024
 // equal steps finds the step that holds the need-th highest of them, between v0 and v1 as it turns out; what lies above
 // v1 + 2 eps is taken, what lies below v0 - 2 eps is not, and the few between are scored in fp64 and ranked by
 // counting.  (All scores in fp64, on the fp64 matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for either
@@ -29,7 +29,6 @@ namespace zgcm {
 namespace {
 
 constexpr int SEL_ROWS = 16;                      // blocks of a warp at a time
-constexpr int SEL_BITS = 10, SEL_BINS = 1 << SEL_BITS;
 constexpr int SEL_LIST = 256;                     // most keys ranked by counting
 
 struct SelectParams {
@@ -79,8 +78,10 @@ template <int WARPS> __device__ __forceinline__ uint32_t cta_scan(uint32_t x, ui
     return before + s - x;
 }
 
+// steps of the histogram: 4 or 8 for each thread
+template <int THREADS> constexpr int kSelBits = THREADS == 256 ? 10 : 12;
+
 struct SelSmem {
-    uint32_t hist[SEL_BINS];
     u64 list[SEL_LIST];
     uint16_t index[SEL_LIST];     // of the list's keys
     u64 lo[16], hi[16];           // lowest and highest of each warp's
@@ -89,7 +90,7 @@ struct SelSmem {
     uint32_t bin, above, count, n_list, need_eq, taken;
     uint32_t mean_max;            // largest |k_mean| as its bits, q's largest 1-norm as fp32 bits
     uint32_t q1;
-    uint32_t v0, v1;              // ordered
+    uint32_t lowest, highest;     // fp32 scores of those that compete, ordered (the highest of all: one is NaN)
 };
 
 // sm.thr and sm.need_eq of the `need` highest keys of the list (n <= SEL_LIST of them, at least `need`)
@@ -113,16 +114,20 @@ __device__ __forceinline__ void rank_list(SelSmem& sm, int n, int need) {
 
 // The step of the histogram, counted from the top, in which the need-th falls: sm.bin, its sm.count and the number
 // sm.above of those in higher steps.  The histogram is left zeroed.
-template <int THREADS> __device__ __forceinline__ void find_step(SelSmem& sm, int need) {
-    constexpr int PER = SEL_BINS / THREADS;
+template <int THREADS> __device__ __forceinline__ void find_step(SelSmem& sm, uint32_t* hist, int need) {
+    constexpr int SEL_BINS = 1 << kSelBits<THREADS>, PER = SEL_BINS / THREADS;
     const int tid = threadIdx.x;
-    uint32_t c[PER], mine = 0;
+    uint32_t c[PER], mine = 0;   // steps SEL_BINS - 1 - (tid * PER + i)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        uint32_t& h = sm.hist[SEL_BINS - 1 - (tid * PER + i)];
-        c[i] = h;
-        h = 0;
-        mine += c[i];
+    for (int i = 0; i < PER; i += 4) {
+        uint4* h = reinterpret_cast<uint4*>(hist + SEL_BINS - 4 - (tid * PER + i));
+        const uint4 x = *h;
+        *h = make_uint4(0u, 0u, 0u, 0u);
+        c[i] = x.w;
+        c[i + 1] = x.z;
+        c[i + 2] = x.y;
+        c[i + 3] = x.x;
+        mine += x.x + x.y + x.z + x.w;
     }
     uint32_t before = cta_scan<THREADS / 32>(mine, sm.red);
 #pragma unroll
@@ -137,38 +142,53 @@ template <int THREADS> __device__ __forceinline__ void find_step(SelSmem& sm, in
     __syncthreads();
 }
 
-// The fp64 score of block `row` (counted from jlo) as an ordered integer, by a warp: -inf for a bad page or a NaN.
+// The fp64 score of block j as an ordered integer, by a warp (4 lanes a head): -inf for a bad page or a NaN.
 template <typename TK>
 __device__ __forceinline__ u64 exact_key(const SelectParams& p, int b, int kvh, int j) {
-    const int lane = threadIdx.x & 31, G = p.Hq / p.c.Hkv;
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, G = p.Hq / p.c.Hkv;
     const int page = kv8_page(p.c, b, j);
     if (page < 0) return ordered(-INFINITY);
-    const TK* m = reinterpret_cast<const TK*>(p.c.kmean) + ((size_t)page * p.c.Hkv + kvh) * kD + 4 * lane;
-    double x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = (double)key_to_float(m[e]);
-    double best = -INFINITY;
+    const uint4* m = reinterpret_cast<const uint4*>(p.c.kmean + 2 * ((size_t)page * p.c.Hkv + kvh) * kD) + c;
+    u64 best = ordered(-INFINITY);
     bool nan = false;
-    for (int h = 0; h < G; ++h) {
-        const TK* q = static_cast<const TK*>(p.q) + ((size_t)b * p.Hq + (size_t)kvh * G + h) * kD + 4 * lane;
-        double a = 0.0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a = fma((double)key_to_float(q[e]), x[e], a);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    for (int h0 = 0; h0 < G; h0 += 8) {
+        const int h = min(h0 + r, G - 1);   // the last one again where there are no more
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const TK*>(p.q) +
+                                                        ((size_t)b * p.Hq + (size_t)kvh * G + h) * kD) + c;
+        double a0 = 0.0, a1 = 0.0;
+        auto add = [&](uint32_t u, uint32_t v) {
+            const float2 f = KeyType<TK>::unpack(u), g = KeyType<TK>::unpack(v);
+            a0 = fma((double)f.x, (double)g.x, a0);
+            a1 = fma((double)f.y, (double)g.y, a1);
+        };
+#pragma unroll 2
+        for (int i = 0; i < 4; ++i) {
+            const uint4 x = m[4 * i], y = q[4 * i];
+            add(x.x, y.x);
+            add(x.y, y.y);
+            add(x.z, y.z);
+            add(x.w, y.w);
+        }
+        double a = a0 + a1;
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
         nan |= isnan(a);
-        best = a > best ? a : best;
+        if (a >= -INFINITY) best = max(best, ordered(a));
     }
-    return ordered(nan ? -INFINITY : best);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    return __any_sync(0xffffffffu, nan) ? ordered(-INFINITY) : best;
 }
 
 template <typename TK, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int WARPS = THREADS / 32;
+    constexpr int WARPS = THREADS / 32, SEL_BITS = kSelBits<THREADS>, SEL_BINS = 1 << SEL_BITS;
     extern __shared__ __align__(16) unsigned char dyn[];
     SelSmem& sm = *reinterpret_cast<SelSmem*>(dyn);
-    float* score = reinterpret_cast<float*>(dyn + sizeof(SelSmem));   // [candidates], of the first CTA
-    u64* key = reinterpret_cast<u64*>(dyn + sizeof(SelSmem));         // the same place, where fp64 scores take over
+    static_assert(sizeof(SelSmem) % 16 == 0, "the histogram is read by 16 bytes");
+    uint32_t* hist = reinterpret_cast<uint32_t*>(dyn + sizeof(SelSmem));
+    float* score = reinterpret_cast<float*>(hist + SEL_BINS);   // [candidates], of the first CTA
+    u64* key = reinterpret_cast<u64*>(hist + SEL_BINS);         // the same place, where fp64 scores take over
     cg::cluster_group cluster = cg::this_cluster();
     const int cs = cluster.num_blocks(), rank = cluster.block_rank();
     const int item = blockIdx.x / cs, b = item / p.c.Hkv, kvh = item % p.c.Hkv;
@@ -178,49 +198,51 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
     // the sequence's page numbers into L2 while its position is read
     for (int i = tid; i < (p.c.NB * 4 + 127) / 128; i += THREADS)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.table + (size_t)b * p.c.NB + min(32 * i, p.c.NB - 1)));
-    for (int i = tid; i < SEL_BINS; i += THREADS) sm.hist[i] = 0;
+    for (int i = tid; i < SEL_BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) {
         sm.mean_max = sm.q1 = 0;
         sm.n_list = sm.taken = 0;
-        sm.v0 = ~0u;
-        sm.v1 = 0u;
+        sm.lowest = ~0u;
+        sm.highest = 0u;
         sm.thr = ~0ULL;
         sm.need_eq = 0;
     }
+    cluster.barrier_arrive();   // shared memory is as above (waited for where it is first written to)
     const int own = pos < 0 ? 0 : pos / kBlk, jlo = pos < 0 ? 0 : max(0, pos - p.W + 1) / kBlk;
     const bool reach = own - jlo < p.c.NB;        // the window's blocks are all in the table
     const int n = reach ? own - jlo : 0;          // candidates jlo .. own - 1
     int* out = p.blocks + (size_t)item * p.n_select;
     if (n <= p.n_select) {                        // the same for every CTA of the cluster
+        cluster.barrier_wait();
         if (rank == 0)
             for (int i = tid; i < p.n_select; i += THREADS) out[i] = i < n ? jlo + i : -1;
         return;
     }
-    if (cs > 1)
-        cluster.sync();   // the first CTA runs, its shared memory is as above
-    else
-        __syncthreads();
     float* dst = cluster.map_shared_rank(score, 0);
     SelSmem& first = *cluster.map_shared_rank(&sm, 0);
     const int per = ((n + cs - 1) / cs + SEL_ROWS - 1) / SEL_ROWS * SEL_ROWS, r0 = min(n, rank * per), r1 = min(n, r0 + per);
-    uint32_t mean_max = 0;
+    const int i0 = p.n_first, i1 = n - p.n_last;   // those that compete: the first and last ones are taken anyhow
+    float q1_max = 0.f;
+    bool ready = false;     // the first CTA's shared memory
+    uint32_t mean_max = 0, lowest = ~0u, highest = 0u;
     for (int h0 = 0; h0 < G; h0 += SEL_ROWS / 2) {
         const int nh = min(SEL_ROWS / 2, G - h0);
-        // the second operand: head r, dims 16 i + 4 c .. + 3
-        uint2 q[8];
+        // the second operand: head r, dims 32 i + 8 c .. + 7 (both operands have the dims in this order)
+        uint4 q[4];
         float q1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            q[i] = make_uint2(0u, 0u);
+        for (int i = 0; i < 4; ++i) {
+            q[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < nh)
-                q[i] = *reinterpret_cast<const uint2*>(static_cast<const TK*>(p.q) +
-                                                       ((size_t)b * p.Hq + (size_t)kvh * G + h0 + r) * kD + 16 * i + 4 * c);
+                q[i] = *reinterpret_cast<const uint4*>(static_cast<const TK*>(p.q) +
+                                                       ((size_t)b * p.Hq + (size_t)kvh * G + h0 + r) * kD + 32 * i + 8 * c);
             const float2 x = KeyType<TK>::unpack(q[i].x), y = KeyType<TK>::unpack(q[i].y);
-            q1 += fabsf(x.x) + fabsf(x.y) + (fabsf(y.x) + fabsf(y.y));
+            const float2 z = KeyType<TK>::unpack(q[i].z), w = KeyType<TK>::unpack(q[i].w);
+            q1 += fabsf(x.x) + fabsf(x.y) + (fabsf(y.x) + fabsf(y.y)) + (fabsf(z.x) + fabsf(z.y) + (fabsf(w.x) + fabsf(w.y)));
         }
         q1 += __shfl_xor_sync(0xffffffffu, q1, 1);
         q1 += __shfl_xor_sync(0xffffffffu, q1, 2);
-        if (rank == 0 && warp == 0 && c == 0) atomicMax(&sm.q1, __float_as_uint(q1));   // positive: bits order as values
+        q1_max = fmaxf(q1_max, q1);
         int pages[2];
         auto look_up = [&](int rows) {
 #pragma unroll
@@ -229,24 +251,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         };
         look_up(r0 + warp * SEL_ROWS);
         for (int rows = r0 + warp * SEL_ROWS; rows < r1; rows += WARPS * SEL_ROWS) {
-            uint2 w[2][8];
+            uint4 w[2][4];
             uint32_t big[2] = {0, 0};
             const bool bad[2] = {pages[0] < 0, pages[1] < 0};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const char* m = p.c.kmean + 2 * (((size_t)max(pages[x], 0) * p.c.Hkv + kvh) * kD + 4 * c);
+                const char* m = p.c.kmean + 2 * (((size_t)max(pages[x], 0) * p.c.Hkv + kvh) * kD + 8 * c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[x][e] = bad[x] ? make_uint2(0u, 0u) : *reinterpret_cast<const uint2*>(m + 32 * e);
+                for (int e = 0; e < 4; ++e)
+                    w[x][e] = bad[x] ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(m + 64 * e);
             }
             look_up(rows + WARPS * SEL_ROWS);   // the next step's, while the means come
+            if (!ready) cluster.barrier_wait();
+            ready = true;
             float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 mma16816<KeyType<TK>::kBf>(d, w[0][e].x, w[1][e].x, w[0][e].y, w[1][e].y, q[e].x, q[e].y);
+                mma16816<KeyType<TK>::kBf>(d, w[0][e].z, w[1][e].z, w[0][e].w, w[1][e].w, q[e].z, q[e].w);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    big[x] = __vmaxu2(big[x], __vmaxu2(w[x][e].x & 0x7fff7fffu, w[x][e].y & 0x7fff7fffu));
+                    big[x] = __vmaxu2(__vmaxu2(big[x], __vmaxu2(w[x][e].x & 0x7fff7fffu, w[x][e].y & 0x7fff7fffu)),
+                                      __vmaxu2(w[x][e].z & 0x7fff7fffu, w[x][e].w & 0x7fff7fffu));
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -265,89 +291,72 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
                 if (row < r1 && !odd) mean_max = max(mean_max, max(big[x] & 0xffffu, big[x] >> 16));
                 if (c == 0 && row < r1) {
                     if (h0 > 0) s = fmaxf(s, dst[row]);
-                    if (odd || (h0 > 0 && isnan(dst[row])) || bad[x]) s = NAN;
-                    dst[row] = s;
+                    odd = odd || (h0 > 0 && isnan(dst[row])) || bad[x];
+                    dst[row] = odd ? NAN : s;
+                    if (h0 + SEL_ROWS / 2 >= G && row >= i0 && row < i1) {
+                        lowest = min(lowest, ordered(s));
+                        highest = max(highest, odd ? ~0u : ordered(s));
+                    }
                 }
             }
         }
     }
+    if (!ready) cluster.barrier_wait();
     mean_max = __reduce_max_sync(0xffffffffu, mean_max);
-    if (lane == 0) atomicMax(&first.mean_max, mean_max);
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    highest = __reduce_max_sync(0xffffffffu, highest);
+    if (rank == 0 && warp == 0 && c == 0) atomicMax(&sm.q1, __float_as_uint(q1_max));   // positive: bits order as values
+    if (lane == 0) {
+        atomicMax(&first.mean_max, mean_max);
+        atomicMin(&first.lowest, lowest);
+        atomicMax(&first.highest, highest);
+    }
     if (cs > 1)
         cluster.sync();
     else
         __syncthreads();
     if (rank != 0) return;
 
-    // of the blocks that compete (the first n_first and last n_last are taken anyhow), `need` are taken
-    int need = p.n_select - p.n_first - p.n_last;
-    const int i0 = p.n_first, i1 = n - p.n_last;
-    bool exact = false;     // keys instead of scores
+    int need = p.n_select - p.n_first - p.n_last;   // of those that compete
     const bool some = need > 0;
+    bool exact = false;     // keys instead of scores
     if (some) {
-        float lo = INFINITY, hi = -INFINITY;
-        bool odd = false;
-        for (int i = i0 + tid; i < i1; i += THREADS) {
-            const float x = score[i];
-            odd |= isnan(x);
-            lo = fminf(lo, x);
-            hi = fmaxf(hi, x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        float* wlo = reinterpret_cast<float*>(sm.lo);
-        float* whi = reinterpret_cast<float*>(sm.hi);
-        if (lane == 0) {
-            wlo[warp] = lo;
-            whi[warp] = hi;
-        }
-        exact = __syncthreads_or(odd);
+        const float lo = from_ordered(sm.lowest), hi = from_ordered(sm.highest);
+        const float width = hi - lo, steps = width > 0.f ? (SEL_BINS - 1) / width : 0.f;
+        exact = !isfinite(width) || !isfinite(steps);   // the same for all threads
         if (!exact) {
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i) {
-                lo = fminf(lo, wlo[i]);
-                hi = fmaxf(hi, whi[i]);
-            }
-            const float width = hi - lo, steps = width > 0.f ? (SEL_BINS - 1) / width : 0.f;
-            exact = !isfinite(width) || !isfinite(steps);   // the same for all threads
-            if (!exact) {
-                auto step = [&](float x) { return min(SEL_BINS - 1, (int)((x - lo) * steps)); };   // grows with x
-                for (int i = i0 + tid; i < i1; i += THREADS) atomicAdd(&sm.hist[step(score[i])], 1u);
-                __syncthreads();
-                find_step<THREADS>(sm, need);
-                const int bin = sm.bin;
-                for (int i = i0 + tid; i < i1; i += THREADS)
-                    if (step(score[i]) == bin) {
-                        atomicMin(&sm.v0, ordered(score[i]));
-                        atomicMax(&sm.v1, ordered(score[i]));
-                    }
-                __syncthreads();
-                const float eps = 0x1p-13f * __uint_as_float(sm.q1) * magnitude<TK>(sm.mean_max) + 0x1p-100f;
-                const float v0 = from_ordered(sm.v0) - 2.f * eps, v1 = from_ordered(sm.v1) + 2.f * eps;
-                // taken, not taken, and the list of those between
-                uint32_t above = 0;
-                for (int i = i0 + tid; i < i1; i += THREADS) {
-                    const float x = score[i];
-                    if (x > v1) {
-                        score[i] = INFINITY;
-                        ++above;
-                    } else if (x < v0) {
-                        score[i] = -INFINITY;
-                    } else {
-                        const uint32_t at = atomicAdd(&sm.n_list, 1u);
-                        if (at < SEL_LIST) sm.index[at] = (uint16_t)i;
-                    }
+            auto step = [&](float x) { return min(SEL_BINS - 1, (int)((x - lo) * steps)); };   // grows with x
+            for (int i = i0 + tid; i < i1; i += THREADS) atomicAdd(&hist[step(score[i])], 1u);
+            __syncthreads();
+            find_step<THREADS>(sm, hist, need);
+            // the step's edges (its own rounding is 2^-12 of a step, theirs less than 2^-22 of a score: within eps)
+            const float eps = 0x1.7p-15f * __uint_as_float(sm.q1) * magnitude<TK>(sm.mean_max) + 0x1p-100f;
+            const float v0 = lo + ((float)sm.bin - 0x1p-11f) * (width / (SEL_BINS - 1)) - 2.f * eps;
+            const float v1 = lo + ((float)sm.bin + (1.f + 0x1p-11f)) * (width / (SEL_BINS - 1)) + 2.f * eps;
+            // taken, not taken, and the list of those between
+            uint32_t above = 0;
+            for (int i = i0 + tid; i < i1; i += THREADS) {
+                const float x = score[i];
+                if (x > v1) {
+                    score[i] = INFINITY;
+                    ++above;
+                } else if (x < v0) {
+                    score[i] = -INFINITY;
+                } else {
+                    const uint32_t at = atomicAdd(&sm.n_list, 1u);
+                    if (at < SEL_LIST) sm.index[at] = (uint16_t)i;
                 }
-                above = __reduce_add_sync(0xffffffffu, above);
-                if (lane == 0) atomicAdd(&sm.taken, above);
-                __syncthreads();
-                const int between = sm.n_list;
-                exact = between > SEL_LIST;
-                if (!exact) {
-                    need -= sm.taken;
+            }
+            above = __reduce_add_sync(0xffffffffu, above);
+            if (lane == 0 && above > 0) atomicAdd(&sm.taken, above);
+            __syncthreads();
+            const int between = sm.n_list;
+            exact = between > SEL_LIST;
+            if (!exact) {
+                need -= sm.taken;
+                if (between == need) {   // all of them: one block is alone there as a rule
+                    if (tid < between) score[sm.index[tid]] = INFINITY;
+                } else {
                     for (int i = warp; i < between; i += WARPS) {
                         const u64 k = exact_key<TK>(p, b, kvh, jlo + sm.index[i]);
                         if (lane == 0) sm.list[i] = k;
@@ -396,9 +405,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
         for (;;) {
             const int shift = max(0, 64 - SEL_BITS - __clzll((long long)range));
             for (int i = i0 + tid; i < i1; i += THREADS)
-                if (key[i] - lo <= range) atomicAdd(&sm.hist[(key[i] - lo) >> shift], 1u);
+                if (key[i] - lo <= range) atomicAdd(&hist[(key[i] - lo) >> shift], 1u);
             __syncthreads();
-            find_step<THREADS>(sm, need);
+            find_step<THREADS>(sm, hist, need);
             need -= sm.above;
             lo += (u64)sm.bin << shift;
             range = (1ULL << shift) - 1;
@@ -462,7 +471,7 @@ template <typename TK, int THREADS> cudaError_t launch(const SelectParams& p, cu
     int cs = 1;
     while (cs < 8 && items * cs < 148 && p.c.NB / (2 * cs) >= THREADS / 4) cs *= 2;
     const int most = p.c.NB < kKv8MaxBlocks ? p.c.NB : kKv8MaxBlocks;
-    const size_t smem = sizeof(SelSmem) + (size_t)most * 8;
+    const size_t smem = sizeof(SelSmem) + (4u << kSelBits<THREADS>) + (size_t)most * 8;
     if (items * cs > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto kernel = kv8_select_kernel<TK, THREADS>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
