@@ -34,7 +34,8 @@ namespace {
 
 constexpr int QR_THREADS = 256;
 constexpr int QR_WARPS = QR_THREADS / 32;
-constexpr int QR_MAX_WPT = 16;           // most warps that share a token's rows
+constexpr int QR_MAX_WPT_LOG = 4;        // at most 16 warps share a token's rows
+constexpr int QR_FWD_CTAS = 444;         // most CTAs of the forward (3 per SM)
 constexpr int QR_BWD_CTAS = 296;         // most CTAs of the backward (2 per SM), one dgamma partial each
 constexpr int kHalf21 = 21;              // the layer's rope_dims / 2
 
@@ -49,7 +50,7 @@ struct QrParams {
     const float* gamma_k;
     const int* pos;
     float* part;                 // backward: [CTAs][2][128] partial dgamma
-    int T, Hq, Hkv, half, wpt;   // wpt: warps of a token
+    int T, Hq, Hkv, half, wpt_log;   // log2 of the warps of a token
     float eps;
     double turns[kMaxHalf];      // rope_base^(-2i/rope_dims) / 2 pi
 };
@@ -156,8 +157,8 @@ template <typename T, bool H21> __device__ __forceinline__ void fill_smem(const 
     __syncthreads();
 }
 
-__device__ __forceinline__ void angles(const QrParams& p, float2* cs, int t) {
-    const double pos = (double)p.pos[t];
+__device__ __forceinline__ void angles(const QrParams& p, float2* cs, int at) {
+    const double pos = (double)at;
     __syncwarp();   // the token before has been read
     for (int j = threadIdx.x & 31; j < p.half; j += 32) {
         const double a = pos * p.turns[j];
@@ -277,57 +278,81 @@ __device__ __forceinline__ void load_row(const Rows& q, const Rows& k, int Hq, i
     }
 }
 
-// A warp takes a token, or one of wpt shares of its rows, q and k counted through, 4 rows at a time and the next 4
+// The walk of a warp over its units: a token, or one of wpt shares of its rows.
+struct Walk {
+    uint32_t unit;
+    int t, h0, pos;   // the unit's token, first row (past the last: no such unit) and position
+    __device__ __forceinline__ explicit Walk(const QrParams& p) : unit(blockIdx.x * QR_WARPS + (threadIdx.x >> 5)) { look(p); }
+    __device__ __forceinline__ bool more(const QrParams& p) const { return unit < (uint32_t)p.T << p.wpt_log; }
+    __device__ __forceinline__ void step(const QrParams& p) {
+        unit += gridDim.x * QR_WARPS;
+        look(p);
+    }
+    __device__ __forceinline__ void look(const QrParams& p) {
+        t = pos = 0;
+        h0 = p.Hq + p.Hkv;
+        if (more(p)) {
+            t = unit >> p.wpt_log;
+            h0 = 4 * (unit & ((1u << p.wpt_log) - 1));
+            pos = p.pos[t];
+        }
+    }
+};
+
+// A warp takes its units' rows, q and k counted through, 4 at a time and the next 4, the next unit's behind the last,
 // already on their way.
 template <typename X, typename Y, bool H21>
 __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const __grid_constant__ QrParams p) {
     __shared__ QrSmem<X, H21> sm;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
     fill_smem(p, sm);
-    const long long unit = (long long)blockIdx.x * QR_WARPS + warp;
-    const int t = (int)(unit / p.wpt), share = (int)(unit % p.wpt);
-    if (t >= p.T) return;
-    const int H = p.Hq + p.Hkv, step = 4 * p.wpt;
-    Vec8<X> next[2];
-    load_row(p.q, p.k, p.Hq, H, next, t, 4 * share + row, l);
-    angles(p, sm.cs[warp], t);
+    const int H = p.Hq + p.Hkv, step = 4 << p.wpt_log;
     const Partner21<X> p21;
-    float2 a[2][4], b[2][4];
-    int side = -1;   // whose factors a, b are
-    for (int base = 4 * share; base < H; base += step) {
-        const int h = base + row;
-        Vec8<X> v[2] = {next[0], next[1]};
-        load_row(p.q, p.k, p.Hq, H, next, t, h + step, l);
-        if (side != (h >= p.Hq)) {
-            side = h >= p.Hq;
-            const float* g = sm.gamma[side];
-            factors<1>(sm.cs[warp], g, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
-            factors<1>(sm.cs[warp], g, 64 + 8 * l, H21 ? kHalf21 : p.half, a[1], b[1]);
-        }
-        float2 f[2][4], y[2][4];
-        v[0].get(f[0]);
-        v[1].get(f[1]);
-        if (H21)
-            p21.get(v[0], y[0]);
-        else
-            partners(v, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
-        float2 ss = sm100::fmul2(f[0][0], f[0][0]);
-#pragma unroll
-        for (int e = 1; e < 8; ++e) ss = sm100::ffma2(f[e >> 2][e & 3], f[e >> 2][e & 3], ss);
-        const float2 r = pair(rsqrtf(sum8(ss.x + ss.y) * (1.0f / kD) + p.eps));
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 z = sm100::fmul2(f[ch][e], a[ch][e]);
-                if (!H21 || ch == 0) z = sm100::ffma2(y[ch][e], b[ch][e], z);
-                f[ch][e] = sm100::fmul2(z, r);
+    Walk at(p);
+    Vec8<X> next[2];
+    load_row(p.q, p.k, p.Hq, H, next, at.t, at.h0 + row, l);
+    while (at.more(p)) {
+        const int t = at.t, h0 = at.h0;
+        angles(p, sm.cs[warp], at.pos);
+        at.step(p);
+        float2 a[2][4], b[2][4];
+        int side = -1;   // whose factors a, b are
+        for (int base = h0; base < H; base += step) {
+            const int h = base + row;
+            Vec8<X> v[2] = {next[0], next[1]};
+            const bool last = base + step >= H;
+            load_row(p.q, p.k, p.Hq, H, next, last ? at.t : t, (last ? at.h0 : base + step) + row, l);
+            if (side != (h >= p.Hq)) {
+                side = h >= p.Hq;
+                const float* g = sm.gamma[side];
+                factors<1>(sm.cs[warp], g, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
+                factors<1>(sm.cs[warp], g, 64 + 8 * l, H21 ? kHalf21 : p.half, a[1], b[1]);
             }
-        if (h < H) {
-            const Rows& o = h < p.Hq ? p.yq : p.yk;
-            const long long at = t * o.ts + (h < p.Hq ? h : h - p.Hq) * o.hs + 8 * l;
-            Vec8<Y>::store(o.p, at, f[0]);
-            Vec8<Y>::store(o.p, at + 64, f[1]);
+            float2 f[2][4], y[2][4];
+            v[0].get(f[0]);
+            v[1].get(f[1]);
+            if (H21)
+                p21.get(v[0], y[0]);
+            else
+                partners(v, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
+            float2 ss = sm100::fmul2(f[0][0], f[0][0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) ss = sm100::ffma2(f[e >> 2][e & 3], f[e >> 2][e & 3], ss);
+            const float2 r = pair(rsqrtf(sum8(ss.x + ss.y) * (1.0f / kD) + p.eps));
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 z = sm100::fmul2(f[ch][e], a[ch][e]);
+                    if (!H21 || ch == 0) z = sm100::ffma2(y[ch][e], b[ch][e], z);
+                    f[ch][e] = sm100::fmul2(z, r);
+                }
+            if (h < H) {
+                const Rows& o = h < p.Hq ? p.yq : p.yk;
+                const long long to = t * o.ts + (h < p.Hq ? h : h - p.Hq) * o.hs + 8 * l;
+                Vec8<Y>::store(o.p, to, f[0]);
+                Vec8<Y>::store(o.p, to + 64, f[1]);
+            }
         }
     }
 }
@@ -338,30 +363,34 @@ template <typename X, typename Y, bool H21>
 __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QrParams p) {
     __shared__ QrSmem<Y, H21> sm;
     __shared__ float4 dgk[QR_WARPS][4][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the sum of the partials may take its place early
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
     fill_smem(p, sm);
     float2 dg[2][4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) dgk[warp][i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     const Partner21<Y> p21;
-    const int H = p.Hq + p.Hkv, step = 4 * p.wpt;
-    const long long units = (long long)p.T * p.wpt;
-    for (long long unit = (long long)blockIdx.x * QR_WARPS + warp; unit < units; unit += (long long)gridDim.x * QR_WARPS) {
-        const int t = (int)(unit / p.wpt), share = (int)(unit % p.wpt);
-        Vec8<X> nv[2];
-        Vec8<Y> nw[2];
-        load_row(p.q, p.k, p.Hq, H, nv, t, 4 * share + row, l);
-        load_row(p.yq, p.yk, p.Hq, H, nw, t, 4 * share + row, l);
+    const int H = p.Hq + p.Hkv, step = 4 << p.wpt_log;
+    Walk at(p);
+    Vec8<X> nv[2];
+    Vec8<Y> nw[2];
+    load_row(p.q, p.k, p.Hq, H, nv, at.t, at.h0 + row, l);
+    load_row(p.yq, p.yk, p.Hq, H, nw, at.t, at.h0 + row, l);
+    while (at.more(p)) {
+        const int t = at.t, h0 = at.h0;
         float2 a[2][4], b[2][4];
-        angles(p, sm.cs[warp], t);
+        angles(p, sm.cs[warp], at.pos);
+        at.step(p);
         factors<-1>(sm.cs[warp], nullptr, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
         if (!H21) factors<-1>(sm.cs[warp], nullptr, 64 + 8 * l, p.half, a[1], b[1]);
-        for (int base = 4 * share; base < H; base += step) {
+        for (int base = h0; base < H; base += step) {
             const int h = base + row;
             const Vec8<X> v[2] = {nv[0], nv[1]};
             const Vec8<Y> w[2] = {nw[0], nw[1]};
-            load_row(p.q, p.k, p.Hq, H, nv, t, h + step, l);
-            load_row(p.yq, p.yk, p.Hq, H, nw, t, h + step, l);
+            const bool last = base + step >= H;
+            const int nt = last ? at.t : t, nh = (last ? at.h0 : base + step) + row;
+            load_row(p.q, p.k, p.Hq, H, nv, nt, nh, l);
+            load_row(p.yq, p.yk, p.Hq, H, nw, nt, nh, l);
             float2 f[2][4], u[2][4], y[2][4], ug[2][4];
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
@@ -389,7 +418,7 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
             if (h < H) {
                 const bool isq = h < p.Hq;
                 const Rows& o = isq ? p.dq : p.dk;
-                const long long at = t * o.ts + (isq ? h : h - p.Hq) * o.hs + 8 * l;
+                const long long to = t * o.ts + (isq ? h : h - p.Hq) * o.hs + 8 * l;
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
 #pragma unroll
@@ -397,7 +426,7 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
                         ug[ch][e] = sm100::fmul2(rr, sm100::ffma2(f[ch][e], m, ug[ch][e]));
                         f[ch][e] = sm100::fmul2(u[ch][e], sm100::fmul2(f[ch][e], rr));       // dgamma's term
                     }
-                    Vec8<X>::store(o.p, at + 64 * ch, ug[ch]);
+                    Vec8<X>::store(o.p, to + 64 * ch, ug[ch]);
                 }
                 if (isq) {
 #pragma unroll
@@ -442,6 +471,7 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
 __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float* part, int n, float* dgamma_q, float* dgamma_k) {
     __shared__ float red[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials
     float a = 0.f;
     for (int i = w; i < n; i += 8) a += part[(size_t)i * 2 * kD + col];
     red[w][lane] = a;
@@ -454,16 +484,16 @@ __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float* part, int n
 
 // Warps of a token: the most that still leaves each its own warp on an SM (16 a SM, 148 SMs), so that a decode
 // step's few tokens spread over the GPU; one for long batches (the angles are formed once a warp).
-int warps_per_token(int T) {
-    int n = QR_MAX_WPT;
-    while (n > 1 && (long long)T * n > 148 * 16) n /= 2;
+int warps_per_token_log(int T) {
+    int n = QR_MAX_WPT_LOG;
+    while (n > 0 && ((long long)T << n) > 148 * 16) --n;
     return n;
 }
 
-int fwd_ctas(int T) { return (int)(((long long)T * warps_per_token(T) + QR_WARPS - 1) / QR_WARPS); }
+int all_ctas(int T) { return (int)((((long long)T << warps_per_token_log(T)) + QR_WARPS - 1) / QR_WARPS); }
 
 int bwd_ctas(int T) {
-    const int n = fwd_ctas(T);
+    const int n = all_ctas(T);
     return n < QR_BWD_CTAS ? n : QR_BWD_CTAS;
 }
 
@@ -473,9 +503,9 @@ cudaError_t launch(const QrParams& p, bool bwd, cudaStream_t stream) {
     constexpr bool fwd16 = sizeof(X) == 2, bwd16 = sizeof(Y) == 2;
     const bool h21 = p.half == kHalf21;
     if (!bwd && fwd16 && h21)
-        qk_norm_rope_fwd_kernel<X, Y, fwd16><<<fwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
+        qk_norm_rope_fwd_kernel<X, Y, fwd16><<<min(all_ctas(p.T), QR_FWD_CTAS), QR_THREADS, 0, stream>>>(p);
     else if (!bwd)
-        qk_norm_rope_fwd_kernel<X, Y, false><<<fwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
+        qk_norm_rope_fwd_kernel<X, Y, false><<<min(all_ctas(p.T), QR_FWD_CTAS), QR_THREADS, 0, stream>>>(p);
     else if (bwd16 && h21)
         qk_norm_rope_bwd_kernel<X, Y, bwd16><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
     else
@@ -531,7 +561,7 @@ void fill(QrParams& p, zgcm_rows q, zgcm_rows k, const float* gamma_q, const flo
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.half = rope_dims / 2;
-    p.wpt = warps_per_token(T);
+    p.wpt_log = warps_per_token_log(T);
     p.eps = eps;
     for (int i = 0; i < kMaxHalf; ++i)
         p.turns[i] = i < p.half ? pow(rope_base, -2.0 * i / rope_dims) * 0.15915494309189535 : 0.0;
@@ -586,8 +616,19 @@ int zgcm_qk_norm_rope_bwd(zgcm_rows q, zgcm_rows k, const float* gamma_q, const 
     p.dk = rows_of(dk);
     p.part = static_cast<float*>(workspace);
     if (launch_types(p, x_type, y_type, true, stream) != cudaSuccess) return ZGCM_ERR_CUDA;
-    qk_dgamma_kernel<<<2 * kD / 32, 256, 0, stream>>>(p.part, bwd_ctas(T), dgamma_q, dgamma_k);
-    return cudaGetLastError() == cudaSuccess ? ZGCM_OK : ZGCM_ERR_CUDA;
+    // on the SMs while the backward's last CTAs still run
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * kD / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_dgamma_kernel, (const float*)p.part, bwd_ctas(T), dgamma_q, dgamma_k) == cudaSuccess
+               ? ZGCM_OK
+               : ZGCM_ERR_CUDA;
 }
 
 }  // extern "C"
