@@ -8,6 +8,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -93,8 +95,10 @@ zgcm_rows rows(const Tensor& t, const char* name, at::ScalarType dtype, at::IntA
     return zgcm_rows{t.data_ptr(), ts, hs};
 }
 
-Tensor fresh(const Tensor& like, at::IntArrayRef shape, at::ScalarType dtype) {
-    return at::empty(shape, like.options().dtype(dtype));
+// on the current device and stream (at::empty, through the dispatcher, took 1.5 us: as long as the launch)
+Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype) {
+    return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                     dtype, std::nullopt);
 }
 
 int to_int(PyObject* o) {   // as the C int the library takes; larger ones are the largest
@@ -224,8 +228,8 @@ PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (given(a[10])) rows(tensor(a[10], "kr", 3), "kr", out, tensor(a[1], "k", 3).sizes(), true);
         const Qk x = qk_inputs(a);
         const Here here(a[11], x.index);
-        const Tensor qr = given(a[9]) ? THPVariable_Unpack(a[9]) : fresh(x.q, {x.T, x.Hq, x.D}, out);
-        const Tensor kr = given(a[10]) ? THPVariable_Unpack(a[10]) : fresh(x.q, {x.T, x.Hkv, x.D}, out);
+        const Tensor qr = given(a[9]) ? THPVariable_Unpack(a[9]) : fresh({x.T, x.Hq, x.D}, out);
+        const Tensor kr = given(a[10]) ? THPVariable_Unpack(a[10]) : fresh({x.T, x.Hkv, x.D}, out);
         on_device(qr, "qr", x.index);
         on_device(kr, "kr", x.index);
         const int st = zgcm_qk_norm_rope_fwd(x.rq, x.rk, x.gamma_q, x.gamma_k, x.pos, (int)x.T, (int)x.Hq, (int)x.Hkv, (int)x.D,
@@ -264,11 +268,11 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (have)
                 g[i] = THPVariable_Unpack(a[10 + i]);
             else
-                g[i] = i < 2 ? fresh(x.q, {x.T, i ? x.Hkv : x.Hq, x.D}, x.dtype) : fresh(x.q, {x.D}, at::kFloat);
+                g[i] = i < 2 ? fresh({x.T, i ? x.Hkv : x.Hq, x.D}, x.dtype) : fresh({x.D}, at::kFloat);
             on_device(g[i], kGrads[i], x.index);
         }
         const int64_t need = (int64_t)zgcm_qk_norm_rope_bwd_workspace_size((int)x.T);
-        const Tensor ws = given(a[14]) ? THPVariable_Unpack(a[14]) : fresh(x.q, {need}, at::kByte);
+        const Tensor ws = given(a[14]) ? THPVariable_Unpack(a[14]) : fresh({need}, at::kByte);
         on_device(ws, "workspace", x.index);
         const int st = zgcm_qk_norm_rope_bwd(x.rq, x.rk, x.gamma_q, x.gamma_k, x.pos, rdqr, rdkr, (int)x.T, (int)x.Hq, (int)x.Hkv,
                                              (int)x.D, x.x_type, y_type, to_int(a[7]), to_double(a[8]), (float)to_double(a[9]),
@@ -358,8 +362,8 @@ PyObject* attn_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (given(a[10])) optional(a[10], "workspace", at::kByte, {tensor(a[10], "workspace", 1).numel()}, c.index);
         const int window = to_int(a[6]), heads = as_int(Hq, "the number of heads");
         const Here here(a[11], c.index);
-        const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh(q, {B, Hq, D}, at::kBFloat16);
-        const Tensor lse = given(a[9]) ? THPVariable_Unpack(a[9]) : fresh(q, {B, Hq}, at::kFloat);
+        const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh({B, Hq, D}, at::kBFloat16);
+        const Tensor lse = given(a[9]) ? THPVariable_Unpack(a[9]) : fresh({B, Hq}, at::kFloat);
         void* ws = nullptr;
         size_t bytes = 0;
         Tensor mine;
@@ -368,7 +372,7 @@ PyObject* attn_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ws = t.data_ptr();
             bytes = (size_t)t.numel();
         } else if ((bytes = zgcm_attn_decode_kv8_workspace_size(c.c, heads, window, n_list)) > 0) {
-            mine = fresh(q, {(int64_t)bytes}, at::kByte);
+            mine = fresh({(int64_t)bytes}, at::kByte);
             ws = mine.data_ptr();
         }
         const int st = zgcm_attn_decode_kv8(c.c, q.const_data_ptr(), g, pos.const_data_ptr<int>(), static_cast<const int*>(blocks),
@@ -392,7 +396,7 @@ PyObject* kv8_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         on_device(pos, "pos", c.index);
         optional(a[8], "out", at::kInt, shape, c.index);
         const Here here(a[9], c.index);
-        const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh(q, shape, at::kInt);
+        const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh(shape, at::kInt);
         const int st = zgcm_kv8_select(c.c, q.const_data_ptr(), pos.const_data_ptr<int>(), as_int(Hq, "the number of heads"), to_int(a[7]), n_select,
                                        to_int(a[5]), to_int(a[6]), out.data_ptr<int>(), here.handle());
         return st == ZGCM_OK ? THPVariable_Wrap(out) : status(st);
