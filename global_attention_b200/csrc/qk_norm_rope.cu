@@ -142,13 +142,21 @@ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 template <typename T> constexpr int kPitch = (kD + kD / 2 + 8) * Vec8<T>::kWords / 8 + 2;
 
 template <typename T, bool H21> struct QrSmem {
+    static constexpr int kTurned = H21 ? 64 : kD;              // the first elements, all the rotated ones among them
     __align__(16) float gamma[2][kD];
-    __align__(16) float2 cs[QR_WARPS][kMaxHalf];               // cosine and sine of the warp's token
+    __align__(16) float partner[2][kTurned];                   // gamma of an element's partner
+    __align__(16) float turn[QR_WARPS][2][kTurned];            // the warp's token: cosines (one where nothing turns), and
+                                                               // sines, as the partner is to be added (zero)
     uint32_t ring[H21 ? 1 : QR_WARPS][4][H21 ? 1 : kPitch<T>]; // [warp][row]: its rotated elements
 };
 
 template <typename T, bool H21> __device__ __forceinline__ void fill_smem(const QrParams& p, QrSmem<T, H21>& sm) {
-    sm.gamma[threadIdx.x >> 7][threadIdx.x & 127] = (threadIdx.x < kD ? p.gamma_q : p.gamma_k)[threadIdx.x & 127];
+    constexpr int N = QrSmem<T, H21>::kTurned;
+    const int d = threadIdx.x & 127, side = threadIdx.x >> 7;
+    const float* g = side ? p.gamma_k : p.gamma_q;
+    sm.gamma[side][d] = g[d];
+    if (d < N) sm.partner[side][d] = d < 2 * p.half ? g[d < p.half ? d + p.half : d - p.half] : 0.f;
+    for (int i = threadIdx.x; i < QR_WARPS * 2 * N; i += QR_THREADS) (&sm.turn[0][0][0])[i] = (i / N) & 1 ? 0.f : 1.f;
     if (!H21) {
         // a lane at the end of the rotated elements reads words that no row writes, against a factor of zero: not NaN
         uint32_t* w = &sm.ring[0][0][0];
@@ -157,39 +165,28 @@ template <typename T, bool H21> __device__ __forceinline__ void fill_smem(const 
     __syncthreads();
 }
 
-__device__ __forceinline__ void angles(const QrParams& p, float2* cs, int at) {
+// cosines and sines of a position into turn[0] and turn[1]; SIGN: 1 forward, -1 back
+template <int SIGN, int N>
+__device__ __forceinline__ void angles(const QrParams& p, float (&turn)[2][N], int at) {
     const double pos = (double)at;
     __syncwarp();   // the token before has been read
     for (int j = threadIdx.x & 31; j < p.half; j += 32) {
         const double a = pos * p.turns[j];
         float sn, co;
         sincospif(2.0f * (float)(a - rint(a)), &sn, &co);
-        cs[j] = make_float2(co, sn);
+        turn[0][j] = turn[0][j + p.half] = co;
+        turn[1][j] = -SIGN * sn;
+        turn[1][j + p.half] = SIGN * sn;
     }
     __syncwarp();
 }
 
-// Factors of the 8 elements from d0: y_d' = y_d a + y_partner b.  gamma (may be null) is that of y; b has the
-// partner's.
-template <int SIGN>
-__device__ __forceinline__ void factors(const float2* cs, const float* gamma, int d0, int half, float2 a[4], float2 b[4]) {
-    float x[8], y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int d = d0 + e;
-        x[e] = gamma ? gamma[d] : 1.f;
-        y[e] = 0.f;
-        if (d < 2 * half) {
-            const float2 w = cs[d < half ? d : d - half];
-            x[e] *= w.x;
-            y[e] = (d < half ? -SIGN : SIGN) * w.y * (gamma ? gamma[d < half ? d + half : d - half] : 1.f);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        a[e] = make_float2(x[2 * e], x[2 * e + 1]);
-        b[e] = make_float2(y[2 * e], y[2 * e + 1]);
-    }
+__device__ __forceinline__ void read8(const float* at, float2 x[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4);
+    x[0] = make_float2(a.x, a.y);
+    x[1] = make_float2(a.z, a.w);
+    x[2] = make_float2(b.x, b.y);
+    x[3] = make_float2(b.z, b.w);
 }
 
 // Partners of the 8 elements of a first chunk, half = 21.  (A lane past the rotated ones gets elements of its own row,
@@ -313,9 +310,9 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
     load_row(p.q, p.k, p.Hq, H, next, at.t, at.h0 + row, l);
     while (at.more(p)) {
         const int t = at.t, h0 = at.h0;
-        angles(p, sm.cs[warp], at.pos);
+        angles<1>(p, sm.turn[warp], at.pos);
         at.step(p);
-        float2 a[2][4], b[2][4];
+        float2 a[2][4], b[2][4];   // y_d' = y_d a + y_partner b, times r
         int side = -1;   // whose factors a, b are
         for (int base = h0; base < H; base += step) {
             const int h = base + row;
@@ -324,9 +321,21 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
             load_row(p.q, p.k, p.Hq, H, next, last ? at.t : t, (last ? at.h0 : base + step) + row, l);
             if (side != (h >= p.Hq)) {
                 side = h >= p.Hq;
-                const float* g = sm.gamma[side];
-                factors<1>(sm.cs[warp], g, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
-                factors<1>(sm.cs[warp], g, 64 + 8 * l, H21 ? kHalf21 : p.half, a[1], b[1]);
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    const int d = 64 * ch + 8 * l;
+                    read8(&sm.gamma[side][d], a[ch]);
+                    if (H21 && ch == 1) break;
+                    float2 co[4], si[4];
+                    read8(&sm.turn[warp][0][d], co);
+                    read8(&sm.turn[warp][1][d], si);
+                    read8(&sm.partner[side][d], b[ch]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[ch][e] = sm100::fmul2(a[ch][e], co[e]);
+                        b[ch][e] = sm100::fmul2(b[ch][e], si[e]);
+                    }
+                }
             }
             float2 f[2][4], y[2][4];
             v[0].get(f[0]);
@@ -359,10 +368,16 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
 
 // As the forward.  dgamma: this lane's 16 sums over its q rows in registers, those over its k rows, a quarter as
 // many in the layer, in shared memory; the CTA's partials at the end.
+template <typename Y, bool H21> struct BwdSmem {
+    QrSmem<Y, H21> s;
+    float4 dgk[QR_WARPS][4][32];
+};
+
 template <typename X, typename Y, bool H21>
 __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QrParams p) {
-    __shared__ QrSmem<Y, H21> sm;
-    __shared__ float4 dgk[QR_WARPS][4][32];
+    extern __shared__ __align__(16) unsigned char dyn[];
+    QrSmem<Y, H21>& sm = reinterpret_cast<BwdSmem<Y, H21>*>(dyn)->s;
+    auto& dgk = reinterpret_cast<BwdSmem<Y, H21>*>(dyn)->dgk;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the sum of the partials may take its place early
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
     fill_smem(p, sm);
@@ -379,10 +394,13 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
     while (at.more(p)) {
         const int t = at.t, h0 = at.h0;
         float2 a[2][4], b[2][4];
-        angles(p, sm.cs[warp], at.pos);
+        angles<-1>(p, sm.turn[warp], at.pos);
         at.step(p);
-        factors<-1>(sm.cs[warp], nullptr, 8 * l, H21 ? kHalf21 : p.half, a[0], b[0]);
-        if (!H21) factors<-1>(sm.cs[warp], nullptr, 64 + 8 * l, p.half, a[1], b[1]);
+#pragma unroll
+        for (int ch = 0; ch < (H21 ? 1 : 2); ++ch) {
+            read8(&sm.turn[warp][0][64 * ch + 8 * l], a[ch]);
+            read8(&sm.turn[warp][1][64 * ch + 8 * l], b[ch]);
+        }
         for (int base = h0; base < H; base += step) {
             const int h = base + row;
             const Vec8<X> v[2] = {nv[0], nv[1]};
@@ -443,8 +461,8 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
         }
     }
     // the CTA's sums, in a fixed order; the angles' place is free then
-    float(*red)[kD] = reinterpret_cast<float(*)[kD]>(sm.cs);
-    static_assert(sizeof(sm.cs) == QR_WARPS * kD * sizeof(float), "one row of 128 sums a warp");
+    float(*red)[kD] = reinterpret_cast<float(*)[kD]>(sm.turn);
+    static_assert(sizeof(sm.turn) >= QR_WARPS * kD * sizeof(float), "one row of 128 sums a warp");
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         __syncthreads();
@@ -497,20 +515,28 @@ int bwd_ctas(int T) {
     return n < QR_BWD_CTAS ? n : QR_BWD_CTAS;
 }
 
-template <typename X, typename Y>
-cudaError_t launch(const QrParams& p, bool bwd, cudaStream_t stream) {
-    // the type whose rows are exchanged: x forward, dy backward
+template <typename X, typename Y, bool H21> cudaError_t launch_fwd(const QrParams& p, cudaStream_t stream) {
+    qk_norm_rope_fwd_kernel<X, Y, H21><<<min(all_ctas(p.T), QR_FWD_CTAS), QR_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename X, typename Y, bool H21> cudaError_t launch_bwd(const QrParams& p, cudaStream_t stream) {
+    auto kernel = qk_norm_rope_bwd_kernel<X, Y, H21>;
+    constexpr size_t smem = sizeof(BwdSmem<Y, H21>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<bwd_ctas(p.T), QR_THREADS, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename X, typename Y> cudaError_t launch(const QrParams& p, bool bwd, cudaStream_t stream) {
+    // by the type whose rows are exchanged: x forward, dy backward
     constexpr bool fwd16 = sizeof(X) == 2, bwd16 = sizeof(Y) == 2;
     const bool h21 = p.half == kHalf21;
-    if (!bwd && fwd16 && h21)
-        qk_norm_rope_fwd_kernel<X, Y, fwd16><<<min(all_ctas(p.T), QR_FWD_CTAS), QR_THREADS, 0, stream>>>(p);
-    else if (!bwd)
-        qk_norm_rope_fwd_kernel<X, Y, false><<<min(all_ctas(p.T), QR_FWD_CTAS), QR_THREADS, 0, stream>>>(p);
-    else if (bwd16 && h21)
-        qk_norm_rope_bwd_kernel<X, Y, bwd16><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
-    else
-        qk_norm_rope_bwd_kernel<X, Y, false><<<bwd_ctas(p.T), QR_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (bwd) return bwd16 && h21 ? launch_bwd<X, Y, bwd16>(p, stream) : launch_bwd<X, Y, false>(p, stream);
+    return fwd16 && h21 ? launch_fwd<X, Y, fwd16>(p, stream) : launch_fwd<X, Y, false>(p, stream);
 }
 
 template <typename X>
