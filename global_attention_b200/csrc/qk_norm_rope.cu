@@ -189,35 +189,31 @@ __device__ __forceinline__ void read8(const float* at, float2 x[4]) {
     x[3] = make_float2(b.z, b.w);
 }
 
-// Partners of the 8 elements of a first chunk, half = 21.  (A lane past the rotated ones gets elements of its own row,
-// against a factor of zero.)
+// Partners of the 8 elements of a first chunk, half = 21: five words of the row, as many shuffles.  Lanes 0 and 1 want
+// elements 21 up, words 2, 3 of the lane two up and 0, 1, 2 of the one three up; lanes 3 to 5 want 21 down, words 1, 2, 3
+// of the lane three down and 0, 1 of the one two down; lane 2 has both kinds, words 2, 3 of lane 4, 0 of lane 5, 0 and 1 of
+// lane 0.  So a shuffle moves one word number, but for the last, where lane 0 sends word 0, lanes 1 and 2 word 1, the
+// others word 2.  (Lanes 6 and 7, and elements 42 to 47, get elements of their own row, against a factor of zero.)
 template <typename T> struct Partner21 {
-    int up2, up3, dn3, dn2;    // lanes of the warp
-    uint32_t first[4];         // the elements of each word that are below 21
+    int l, from0, from1, from23, from4;   // lanes of the warp
     __device__ __forceinline__ Partner21() {
-        const int lane = threadIdx.x & 31, l = lane & 7, row = lane & 24;
-        up2 = row | ((l + 2) & 7);
-        up3 = row | ((l + 3) & 7);
-        dn3 = row | ((l - 3) & 7);
-        dn2 = row | ((l - 2) & 7);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = 8 * l + 2 * i;
-            first[i] = (d < kHalf21 ? 0xffffu : 0u) | (d + 1 < kHalf21 ? 0xffff0000u : 0u);
-        }
+        const int lane = threadIdx.x & 31, row = lane & 24;
+        l = lane & 7;
+        from0 = row | (l < 3 ? l + 3 : l < 6 ? l - 2 : l);
+        from1 = row | (l < 2 ? l + 3 : l == 2 ? 0 : l < 6 ? l - 3 : l);
+        from23 = row | (l < 3 ? l + 2 : l < 6 ? l - 3 : l);
+        from4 = row | (l < 2 ? l + 3 : l < 6 ? l - 2 : l);
     }
     __device__ __forceinline__ void get(const Vec8<T>& v, float2 y[4]) const {
         const uint32_t m = 0xffffffffu;
-        // elements 5 .. 12 from two lanes up
-        const uint32_t p[5] = {__shfl_sync(m, v.word(2), up2), __shfl_sync(m, v.word(3), up2), __shfl_sync(m, v.word(0), up3),
-                               __shfl_sync(m, v.word(1), up3), __shfl_sync(m, v.word(2), up3)};
-        // elements 3 .. 10 from three lanes down
-        const uint32_t q[5] = {__shfl_sync(m, v.word(1), dn3), __shfl_sync(m, v.word(2), dn3), __shfl_sync(m, v.word(3), dn3),
-                               __shfl_sync(m, v.word(0), dn2), __shfl_sync(m, v.word(1), dn2)};
-        uint32_t u[Vec8<T>::kWords];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = (__funnelshift_r(p[i], p[i + 1], 16) & first[i]) | (__funnelshift_r(q[i], q[i + 1], 16) & ~first[i]);
+        const uint32_t s0 = __shfl_sync(m, v.word(0), from0), s1 = __shfl_sync(m, v.word(1), from1),
+                       s2 = __shfl_sync(m, v.word(2), from23), s3 = __shfl_sync(m, v.word(3), from23),
+                       s4 = __shfl_sync(m, l == 0 ? v.word(0) : l < 3 ? v.word(1) : v.word(2), from4);
+        const bool up = l < 3;
+        const uint32_t w0 = up ? s2 : s1, w1 = up ? s3 : s2, w2 = up ? s0 : s3, w3 = l == 2 ? s4 : up ? s1 : s0,
+                       w4 = l == 2 ? s1 : s4;
+        const uint32_t u[4] = {__funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16), __funnelshift_r(w2, w3, 16),
+                               __funnelshift_r(w3, w4, 16)};
         Vec8<T> o;
         o.set(u);
         o.get(y);
@@ -340,7 +336,7 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
             float2 f[2][4], y[2][4];
             v[0].get(f[0]);
             v[1].get(f[1]);
-            if (H21)
+            if constexpr (H21)
                 p21.get(v[0], y[0]);
             else
                 partners(v, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
                 v[ch].get(f[ch]);
                 w[ch].get(u[ch]);
             }
-            if (H21)
+            if constexpr (H21)
                 p21.get(w[0], y[0]);
             else
                 partners(w, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
