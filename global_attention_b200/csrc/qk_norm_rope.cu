@@ -41,7 +41,7 @@ constexpr int kHalf21 = 21;              // the layer's rope_dims / 2
 
 struct Rows {
     char* p;
-    long long ts, hs;   // elements
+    uint32_t ts, hs;   // elements
 };
 
 struct QrParams {
@@ -51,6 +51,7 @@ struct QrParams {
     const int* pos;
     float* part;                 // backward: [CTAs][2][128] partial dgamma
     int T, Hq, Hkv, half, wpt_log;   // log2 of the warps of a token
+    int fours_q, fours;              // fours of rows of a token's q, of both
     float eps;
     double turns[kMaxHalf];      // rope_base^(-2i/rope_dims) / 2 pi
 };
@@ -258,14 +259,27 @@ __device__ __forceinline__ void partners(const Vec8<T> (&v)[2], float2 (&y)[2][4
     }
 }
 
-// Row h of a token's q and k counted through: nothing past the last.
+// Rows of a token are taken in fours, those of q and then those of k.
+struct Four {
+    bool isq, valid;
+    int h;            // this lane's row
+    __device__ __forceinline__ Four(const QrParams& p, int g, int row) {
+        isq = g < p.fours_q;
+        h = 4 * (isq ? g : g - p.fours_q) + row;
+        valid = h < (isq ? p.Hq : p.Hkv);
+    }
+    __device__ __forceinline__ long long at(const Rows& x, int t, int l) const {
+        return (long long)((unsigned long long)(uint32_t)t * x.ts + (unsigned long long)(uint32_t)h * x.hs + 8 * l);
+    }
+};
+
 template <typename X>
-__device__ __forceinline__ void load_row(const Rows& q, const Rows& k, int Hq, int H, Vec8<X> (&v)[2], int t, int h, int l) {
+__device__ __forceinline__ void load_row(const Rows& q, const Rows& k, const Four& f, Vec8<X> (&v)[2], int t, int l) {
     v[0].zero();
     v[1].zero();
-    if (h < H) {
-        const Rows& x = h < Hq ? q : k;
-        const long long at = t * x.ts + (h < Hq ? h : h - Hq) * x.hs + 8 * l;
+    if (f.valid) {
+        const Rows& x = f.isq ? q : k;
+        const long long at = f.at(x, t, l);
         v[0].load(x.p, at);
         v[1].load(x.p, at + 64);
     }
@@ -274,7 +288,7 @@ __device__ __forceinline__ void load_row(const Rows& q, const Rows& k, int Hq, i
 // The walk of a warp over its units: a token, or one of wpt shares of its rows.
 struct Walk {
     uint32_t unit;
-    int t, h0, pos;   // the unit's token, first row (past the last: no such unit) and position
+    int t, g, pos;   // the unit's token, first four (past the last: no such unit) and position
     __device__ __forceinline__ explicit Walk(const QrParams& p) : unit(blockIdx.x * QR_WARPS + (threadIdx.x >> 5)) { look(p); }
     __device__ __forceinline__ bool more(const QrParams& p) const { return unit < (uint32_t)p.T << p.wpt_log; }
     __device__ __forceinline__ void step(const QrParams& p) {
@@ -283,10 +297,10 @@ struct Walk {
     }
     __device__ __forceinline__ void look(const QrParams& p) {
         t = pos = 0;
-        h0 = p.Hq + p.Hkv;
+        g = p.fours;
         if (more(p)) {
             t = unit >> p.wpt_log;
-            h0 = 4 * (unit & ((1u << p.wpt_log) - 1));
+            g = unit & ((1u << p.wpt_log) - 1);
             pos = p.pos[t];
         }
     }
@@ -299,24 +313,24 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
     __shared__ QrSmem<X, H21> sm;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, row = lane >> 3;
     fill_smem(p, sm);
-    const int H = p.Hq + p.Hkv, step = 4 << p.wpt_log;
+    const int step = 1 << p.wpt_log;
     const Partner21<X> p21;
     Walk at(p);
     Vec8<X> next[2];
-    load_row(p.q, p.k, p.Hq, H, next, at.t, at.h0 + row, l);
+    load_row(p.q, p.k, Four(p, at.g, row), next, at.t, l);
     while (at.more(p)) {
-        const int t = at.t, h0 = at.h0;
+        const int t = at.t, g0 = at.g;
         angles<1>(p, sm.turn[warp], at.pos);
         at.step(p);
         float2 a[2][4], b[2][4];   // y_d' = y_d a + y_partner b, times r
         int side = -1;   // whose factors a, b are
-        for (int base = h0; base < H; base += step) {
-            const int h = base + row;
+        for (int g = g0; g < p.fours; g += step) {
+            const Four four(p, g, row);
             Vec8<X> v[2] = {next[0], next[1]};
-            const bool last = base + step >= H;
-            load_row(p.q, p.k, p.Hq, H, next, last ? at.t : t, (last ? at.h0 : base + step) + row, l);
-            if (side != (h >= p.Hq)) {
-                side = h >= p.Hq;
+            const bool last = g + step >= p.fours;
+            load_row(p.q, p.k, Four(p, last ? at.g : g + step, row), next, last ? at.t : t, l);
+            if (side != !four.isq) {
+                side = !four.isq;
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
                     const int d = 64 * ch + 8 * l;
@@ -352,9 +366,9 @@ __global__ void __launch_bounds__(QR_THREADS, 3) qk_norm_rope_fwd_kernel(const _
                     if (!H21 || ch == 0) z = sm100::ffma2(y[ch][e], b[ch][e], z);
                     f[ch][e] = sm100::fmul2(z, r);
                 }
-            if (h < H) {
-                const Rows& o = h < p.Hq ? p.yq : p.yk;
-                const long long to = t * o.ts + (h < p.Hq ? h : h - p.Hq) * o.hs + 8 * l;
+            if (four.valid) {
+                const Rows& o = four.isq ? p.yq : p.yk;
+                const long long to = four.at(o, t, l);
                 Vec8<Y>::store(o.p, to, f[0]);
                 Vec8<Y>::store(o.p, to + 64, f[1]);
             }
@@ -381,14 +395,14 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
 #pragma unroll
     for (int i = 0; i < 4; ++i) dgk[warp][i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     const Partner21<Y> p21;
-    const int H = p.Hq + p.Hkv, step = 4 << p.wpt_log;
+    const int step = 1 << p.wpt_log;
     Walk at(p);
     Vec8<X> nv[2];
     Vec8<Y> nw[2];
-    load_row(p.q, p.k, p.Hq, H, nv, at.t, at.h0 + row, l);
-    load_row(p.yq, p.yk, p.Hq, H, nw, at.t, at.h0 + row, l);
+    load_row(p.q, p.k, Four(p, at.g, row), nv, at.t, l);
+    load_row(p.yq, p.yk, Four(p, at.g, row), nw, at.t, l);
     while (at.more(p)) {
-        const int t = at.t, h0 = at.h0;
+        const int t = at.t, g0 = at.g;
         float2 a[2][4], b[2][4];
         angles<-1>(p, sm.turn[warp], at.pos);
         at.step(p);
@@ -397,14 +411,14 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
             read8(&sm.turn[warp][0][64 * ch + 8 * l], a[ch]);
             read8(&sm.turn[warp][1][64 * ch + 8 * l], b[ch]);
         }
-        for (int base = h0; base < H; base += step) {
-            const int h = base + row;
+        for (int g = g0; g < p.fours; g += step) {
+            const Four four(p, g, row);
             const Vec8<X> v[2] = {nv[0], nv[1]};
             const Vec8<Y> w[2] = {nw[0], nw[1]};
-            const bool last = base + step >= H;
-            const int nt = last ? at.t : t, nh = (last ? at.h0 : base + step) + row;
-            load_row(p.q, p.k, p.Hq, H, nv, nt, nh, l);
-            load_row(p.yq, p.yk, p.Hq, H, nw, nt, nh, l);
+            const bool last = g + step >= p.fours;
+            const Four next(p, last ? at.g : g + step, row);
+            load_row(p.q, p.k, next, nv, last ? at.t : t, l);
+            load_row(p.yq, p.yk, next, nw, last ? at.t : t, l);
             float2 f[2][4], u[2][4], y[2][4], ug[2][4];
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
@@ -415,24 +429,23 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
                 p21.get(w[0], y[0]);
             else
                 partners(w, y, sm.ring[H21 ? 0 : warp][row], l, p.half);
-            const float* g = sm.gamma[h < p.Hq ? 0 : 1] + 8 * l;
+            const float* gamma = sm.gamma[four.isq ? 0 : 1] + 8 * l;
             float2 ss = pair(0.f), sx = pair(0.f);
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (!H21 || ch == 0) u[ch][e] = sm100::ffma2(y[ch][e], b[ch][e], sm100::fmul2(u[ch][e], a[ch][e]));
-                    ug[ch][e] = sm100::fmul2(u[ch][e], *reinterpret_cast<const float2*>(g + 64 * ch + 2 * e));
+                    ug[ch][e] = sm100::fmul2(u[ch][e], *reinterpret_cast<const float2*>(gamma + 64 * ch + 2 * e));
                     ss = sm100::ffma2(f[ch][e], f[ch][e], ss);
                     sx = sm100::ffma2(f[ch][e], ug[ch][e], sx);
                 }
             const float sq = sum8(ss.x + ss.y), sd = sum8(sx.x + sx.y);
             const float r = rsqrtf(sq * (1.0f / kD) + p.eps);
             const float2 m = pair(-r * r * sd * (1.0f / kD)), rr = pair(r);     // m = -r mean(gamma u xhat)
-            if (h < H) {
-                const bool isq = h < p.Hq;
-                const Rows& o = isq ? p.dq : p.dk;
-                const long long to = t * o.ts + (isq ? h : h - p.Hq) * o.hs + 8 * l;
+            if (four.valid) {
+                const Rows& o = four.isq ? p.dq : p.dk;
+                const long long to = four.at(o, t, l);
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
 #pragma unroll
@@ -442,7 +455,7 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
                     }
                     Vec8<X>::store(o.p, to + 64 * ch, ug[ch]);
                 }
-                if (isq) {
+                if (four.isq) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dg[e >> 2][e & 3] = sm100::fadd2(dg[e >> 2][e & 3], f[e >> 2][e & 3]);
                 } else {
@@ -558,6 +571,8 @@ int check(const float* gamma_q, const float* gamma_k, const int* pos, int T, int
     if (!(eps >= 0.f) || !isfinite(eps)) return ZGCM_ERR_INVALID_ARG;
     if (D != kD) return ZGCM_ERR_UNSUPPORTED;
     if ((long double)T * (Hq > Hkv ? Hq : Hkv) * D >= (long double)(1ULL << 40)) return ZGCM_ERR_UNSUPPORTED;
+    for (const zgcm_rows& r : rows)
+        if (r.t_stride < 0 || r.h_stride < 0 || r.t_stride > 0xffffffffLL || r.h_stride > 0xffffffffLL) return ZGCM_ERR_UNSUPPORTED;
     if (T == 0) return ZGCM_OK;
     if (!gamma_q || !gamma_k || !pos) return ZGCM_ERR_INVALID_ARG;
     for (const zgcm_rows& r : rows)
@@ -569,7 +584,7 @@ int check(const float* gamma_q, const float* gamma_k, const int* pos, int T, int
     return ZGCM_OK;
 }
 
-Rows rows_of(const zgcm_rows& r) { return Rows{static_cast<char*>(r.ptr), r.t_stride, r.h_stride}; }
+Rows rows_of(const zgcm_rows& r) { return Rows{static_cast<char*>(r.ptr), (uint32_t)r.t_stride, (uint32_t)r.h_stride}; }
 
 void fill(QrParams& p, zgcm_rows q, zgcm_rows k, const float* gamma_q, const float* gamma_k, const int* pos, int T,
           int Hq, int Hkv, int rope_dims, double rope_base, float eps) {
@@ -584,6 +599,8 @@ void fill(QrParams& p, zgcm_rows q, zgcm_rows k, const float* gamma_q, const flo
     p.Hkv = Hkv;
     p.half = rope_dims / 2;
     p.wpt_log = warps_per_token_log(T);
+    p.fours_q = (Hq + 3) / 4;
+    p.fours = p.fours_q + (Hkv + 3) / 4;
     p.eps = eps;
     for (int i = 0; i < kMaxHalf; ++i)
         p.turns[i] = i < p.half ? pow(rope_base, -2.0 * i / rope_dims) * 0.15915494309189535 : 0.0;

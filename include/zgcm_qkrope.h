@@ -19,7 +19,8 @@
  * brings its own position, pos int32 [T] on the device, any value).  Rows are given by
  * zgcm_rows: element (t, h, d) of a tensor is at ptr + (t * t_stride + h * h_stride + d)
  * elements, so the parts of a packed projection [T, (Hq + 2 Hkv + ...) * D] are read and
- * written in place; strides are multiples of 8 elements and pointers 16-byte aligned.
+ * written in place; strides are multiples of 8 elements from 0 to 2^32 - 1 (larger or negative
+ * ones: ZGCM_ERR_UNSUPPORTED) and pointers 16-byte aligned.
  * Rows of one tensor must not overlap in an output, and outputs must not alias inputs.
  * Types (zgcm_dtype): q, k, dq, dk have x_type; qr, kr, dqr, dkr have y_type; gamma fp32 [D].
  * Arithmetic is fp32 (angles are formed and reduced in fp64); each output element is

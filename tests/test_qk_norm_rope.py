@@ -64,6 +64,8 @@ def test_refuses_pointers(lib, bwd):
         assert _c(lib, bwd, bad=n, ptr=0) == -1
         assert _c(lib, bwd, bad=n, ptr=P + 8) == -3
         assert _c(lib, bwd, bad=n, ptr=P, stride=12) == -3
+        assert _c(lib, bwd, bad=n, ptr=P, stride=2 ** 32) == -2
+        assert _c(lib, bwd, bad=n, ptr=P, stride=-512) == -2
     for n in (range(10, 15) if bwd else range(10, 13)):
         assert _c(lib, bwd, bad=n, ptr=0) == -1
         assert _c(lib, bwd, bad=n, ptr=P + 4) == -3
