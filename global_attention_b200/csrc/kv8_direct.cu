@@ -3,7 +3,7 @@
 // kernel of long ones.
 //
 // There the whole call is a few microseconds, most of them latencies in a row: position, page number, codes.  So a
-// cluster of 1 to 8 CTAs takes an item whose units are split evenly among them; nothing but its own position
+// cluster of 1 to 16 CTAs takes an item whose units are split evenly among them; nothing but its own position
 // decides a CTA's work, the rows of q and of the tail load while page numbers do, the CTAs' parts meet in
 // shared memory across the cluster (each is sent its share of all, and finishes it), and there is no second kernel.  Four CTAs of
 // four warps fit on an SM: their latencies overlap.
@@ -17,6 +17,7 @@ namespace zgcm {
 namespace {
 
 constexpr int DD_THREADS = 128;
+constexpr int DD_SPLIT = 16;                // most CTAs of an item (clusters above 8 have to be allowed)
 constexpr int DD_WAIT = 0x820;
 constexpr size_t DD_RING = 4 * kSlots * kSlot;
 static_assert(DD_RING >= 4 * DK_HEADS * (kD + 4) * sizeof(float), "the warps' parts take the ring's place");
@@ -26,7 +27,7 @@ constexpr int DD_ROW = kD + 4;   // floats of a head in a warp's part: the lanes
 struct DirectSmem {
     WarpSmem warp[4];
     float ml[4][DK_HEADS][2];
-    float from_ml[8][DK_HEADS][2];      // [CTA of the cluster]: its maximum and sum
+    float from_ml[DD_SPLIT][DK_HEADS][2];      // [CTA of the cluster]: its maximum and sum
     float4 from[256];                   // [CTA][place of this CTA's share]: its O
     int abort;
 };
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
             cluster.map_shared_rank(sm.from, at / share)[rank * share + at % share] = x;
         }
     }
+    static_assert(DK_HEADS * DD_SPLIT <= DD_THREADS, "a thread for each head and CTA");
     if (p.split > 1) {
         if (tid < DK_HEADS * p.split) {   // every CTA's copy of the maximum and sum
             const int h = tid % DK_HEADS;
@@ -156,10 +158,10 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
             m = -INFINITY;
             l = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < DD_SPLIT; ++i)
                 if (i < p.split) m = fmaxf(m, sm.from_ml[i][h][0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < DD_SPLIT; ++i)
                 if (i < p.split) {
                     const float2 ml = *reinterpret_cast<const float2*>(sm.from_ml[i][h]);
                     const float4 y = sm.from[i * share + tid];
@@ -180,6 +182,8 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
     const size_t smem = DD_RING + 1024;
     cudaError_t e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (p.split > 8) e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * p.HT * p.split));
     cfg.blockDim = dim3(DD_THREADS);
@@ -197,11 +201,19 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
 }  // namespace
 
 // Whether this kernel takes the call, and how an item is split.  units: the most an item can have.
+//
+// An item is split while there are CTA places left on the 148 SMs (two CTAs an SM) and a CTA keeps more than one unit; the
+// kernel takes the call while a CTA has at most 64 units, or 32 where the CTAs do not fill the SMs, which the equal runs
+// of kv8_decode_kernel do whatever the items.  Measured (us; 8 KV heads of 4, int8, this kernel / that one):
+//   1 sequence of     1000 7.6 / 12.8, 16K 20.7 / 29.6, 32K (31 units a CTA) 32.7 / 36.5, 64K with 8 CTAs an item 96 / 50
+//   16 sequences of   8K (63 units a CTA) 60 / 65, 16K 113 / 108
+//   64 of up to       4K (65) 81 / 87, 8K 156 / 154, 16K 299 / 280: lengths differ, and the longest item decides
+// and 16 CTAs an item against 8: 1 x 4K 10.8 / 12.3, 1 x 16K 20.7 / 29.4.
 bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
-    while (p.split < 8 && items * p.split * 2 <= 296 && units > 2 * p.split) p.split *= 2;
-    return units <= 64 * p.split;
+    while (p.split < DD_SPLIT && items * p.split * 2 <= 296 && units > 2 * p.split) p.split *= 2;
+    return units <= (items * p.split >= 148 ? 64 : 32) * p.split;
 }
 
 cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream) {

@@ -9,10 +9,10 @@
 // need them: the tensor cores give every score in fp32 (16 blocks by 8 heads an instruction), off by less than
 //      eps = 2^-14.5 max_h |q_h|_1 max_j |k_mean_j|_max
 // (8 sums of 17 terms, each off by 2^-22 of the largest of them at most: 2^-14.9 of the terms' sum; the histogram's own roundings are small against the rest); one histogram of 1024
-// equal steps finds the step that holds the need-th highest of them, between v0 and v1 as it turns out; what lies above
+// or 4096 equal steps finds the step that holds the need-th highest of them, whose edges are v0 and v1; what lies above
 // v1 + 2 eps is taken, what lies below v0 - 2 eps is not, and the few between are scored in fp64 and ranked by
-// counting.  (All scores in fp64, on the fp64 matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for either
-// of the benchmark's shapes against NNN.)  Where more than 256 are between, many equal scores say, or a score
+// counting.  (All scores in fp64, on the fp64 matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for 32 of
+// up to 256 blocks of 64 x 8 items, or 64 of 4096 of 2 x 8, against 14.5 and 18.1 here.)  Where more than 256 are between, many equal scores say, or a score
 // is not finite, all are scored in fp64 and the histogram is taken of those (as ordered 64-bit integers), as often as one step
 // of it holds too many.
 //
@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
 
 template <typename TK, int THREADS> cudaError_t launch(const SelectParams& p, cudaStream_t stream) {
     const long long items = (long long)p.c.B * p.c.Hkv;
-    // CTAs of a cluster: one once the (sequence, head) pairs fill the SMs, else up to 8, with at least two steps of 8
-    // rows for each warp left
+    // CTAs of a cluster: one once the (sequence, head) pairs fill the SMs, else up to 8, with a step of 16 rows for half of
+    // the warps left at least (2 sequences of 256K with 1, 2, 4, 8 CTAs: 36.5, 24.6, 18.2, 18.2 us; 64 of 16K with 1, 2:
+    // 14.5, 21.2)
     int cs = 1;
     while (cs < 8 && items * cs < 148 && p.c.NB / (2 * cs) >= THREADS / 4) cs *= 2;
     const int most = p.c.NB < kKv8MaxBlocks ? p.c.NB : kKv8MaxBlocks;
@@ -490,9 +491,11 @@ template <typename TK, int THREADS> cudaError_t launch(const SelectParams& p, cu
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Threads of a CTA: 256 for contexts of up to 512 blocks (four CTAs an SM), else 512.
+// Threads of a CTA: 256 for contexts of up to 1024 blocks (four CTAs an SM), else 512, since one CTA goes through all of an
+// item's scores.  Measured (us, 256 / 512): 64 sequences of 16K 14.5 / 23, of 64K 38 / 47, 16 of 128K 28.8 / 26.0, 8 of
+// 256K 31.4 / 27.2, 2 of 512K 36.3 / 27.5.
 template <typename TK> cudaError_t launch_threads(const SelectParams& p, cudaStream_t stream) {
-    return p.c.NB <= 512 ? launch<TK, 256>(p, stream) : launch<TK, 512>(p, stream);
+    return p.c.NB <= 1024 ? launch<TK, 256>(p, stream) : launch<TK, 512>(p, stream);
 }
 
 }  // namespace
