@@ -382,7 +382,7 @@ def test_decode_lengths(cuda, code, key):
 
 @gpu
 @pytest.mark.parametrize("code,key", [("e4m3", "fp16"), ("int8", "bf16")])
-@pytest.mark.parametrize("B,Hq,Hkv,longest", [(1, 4, 1, 40000), (3, 12, 1, 36000), (90, 8, 2, 4700), (300, 1, 1, 4500)])
+@pytest.mark.parametrize("B,Hq,Hkv,longest", [(1, 4, 1, 40000), (1, 4, 1, 30000), (2, 8, 2, 9000), (3, 12, 1, 36000), (90, 8, 2, 4700), (300, 1, 1, 4500)])
 def test_decode_long_and_many(cuda, code, key, B, Hq, Hkv, longest):
     """Contexts of hundreds of blocks, and more sequences than an SM count: runs that begin and end inside
     sequences, short ones among long ones, idle ones."""
@@ -586,11 +586,12 @@ def test_select_long_contexts(cuda, blocks):
 
 
 @gpu
-def test_select_ties_and_specials(cuda):
-    c = _new(1, 700, 2, "e4m3", "bf16", garbage=False)
+@pytest.mark.parametrize("blocks", [700, 1500])
+def test_select_ties_and_specials(cuda, blocks):
+    c = _new(1, blocks, 2, "e4m3", "bf16", garbage=False)
     q, _ = _queries(1, 4, "bf16")
     c.k_mean.zero_()                                   # every score 0 (and -0)
-    _check_select(c, q, [44800], 9, 1, 1)
+    _check_select(c, q, [64 * blocks], 9, 1, 1)
     _means(c, seed=3)
     page = c.table[0].long()
     c.k_mean[page[100:400:3]] = c.k_mean[page[5]].clone()      # ties across slices
@@ -598,8 +599,8 @@ def test_select_ties_and_specials(cuda):
     c.k_mean[page[18], 0, 0] = float("inf")
     c.k_mean[page[19], :, 5] = float("-inf")
     for n in (3, 40, 90, 200, 699):
-        _check_select(c, q, [44800], n, 0, 0)
-        _check_select(c, q, [44800], n, 1, 1)
+        _check_select(c, q, [64 * blocks], n, 0, 0)
+        _check_select(c, q, [64 * blocks], n, 1, 1)
 
 
 # ------------------------------------------------------------------- together, streams, graphs
