@@ -756,6 +756,8 @@ class ZgcmKv8Cache:
         _need(k_tail, "k_tail", k_tail.dtype, (n_seq, Hkv, KV8_BLOCK, D))
         _need(v_tail, "v_tail", torch.bfloat16, (n_seq, Hkv, KV8_BLOCK, D))
         _need(table, "table", torch.int32, (n_seq, n_blocks))
+        if max(P, n_seq, n_blocks, Hkv) > 2 ** 31 - 1:
+            raise TypeError("the cache is too large")
         tensors = (k_codes, v_codes, k_scale, v_scale, k_mean, k_tail, v_tail, table)
         _one_device(*zip(self._NAMES, tensors))
         self._t = dict(zip(self._NAMES, tensors))
@@ -764,6 +766,7 @@ class ZgcmKv8Cache:
         self._c = _Kv8Struct(*(t.data_ptr() for t in tensors), n_seq, n_blocks, P, Hkv, D,
                              0 if k_codes.dtype == torch.float8_e4m3fn else 1, 0 if k_tail.dtype == torch.bfloat16 else 1)
         self._handle = ctypes.addressof(self._c), k_codes
+        self._memory = [t.untyped_storage() for t in tensors]   # what _c points to, whatever becomes of the tensors
 
     def __getattr__(self, name):
         t = self.__dict__.get("_t", {})

@@ -154,11 +154,8 @@ template <typename F> PyObject* guarded(F&& f) {
     } catch (const Refused& e) {
         PyErr_SetString(PyExc_TypeError, e.what.c_str());
         return nullptr;
-    } catch (python_error& e) {
-        e.restore();
-        return nullptr;
-    } catch (const std::exception& e) {   // torch's: out of memory
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {   // Python's own, torch's (out of memory)
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }
@@ -397,8 +394,8 @@ PyObject* kv8_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         optional(a[8], "out", at::kInt, shape, c.index);
         const Here here(a[9], c.index);
         const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh(shape, at::kInt);
-        const int st = zgcm_kv8_select(c.c, q.const_data_ptr(), pos.const_data_ptr<int>(), as_int(Hq, "the number of heads"), to_int(a[7]), n_select,
-                                       to_int(a[5]), to_int(a[6]), out.data_ptr<int>(), here.handle());
+        const int st = zgcm_kv8_select(c.c, q.const_data_ptr(), pos.const_data_ptr<int>(), as_int(Hq, "the number of heads"),
+                                       to_int(a[7]), n_select, to_int(a[5]), to_int(a[6]), out.data_ptr<int>(), here.handle());
         return st == ZGCM_OK ? THPVariable_Wrap(out) : status(st);
     });
 }
