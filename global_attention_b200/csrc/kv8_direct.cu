@@ -211,7 +211,8 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
 //   1 sequence of     1000 7.6 / 12.8, 16K 20.7 / 29.6, 32K (31 units a CTA) 32.7 / 36.5, 64K with 8 CTAs an item 96 / 50
 //   16 sequences of   8K (63 units a CTA) 60 / 65, 16K 113 / 108
 //   64 of up to       4K (65) 81 / 87, 8K 156 / 154, 16K 299 / 280: lengths differ, and the longest item decides
-// and 16 CTAs an item against 8: 1 x 4K 10.8 / 12.3, 1 x 16K 20.7 / 29.4.
+// and 16 CTAs an item against 8: 1 x 4K 10.8 / 12.3, 1 x 16K 20.7 / 29.4; two CTAs an SM against four: 4 x 16K 35 / 47,
+// 32 listed blocks of 16 sequences 24.9 / 25.2.
 bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
