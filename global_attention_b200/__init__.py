@@ -673,7 +673,8 @@ def zgcm_proj_out_bwd(a, w_o, dy, *, da=None, dw=None, stream=None):
 #
 # The calls of a decode step check their tensors in csrc/torch_calls.cpp (the module _calls), by the
 # same rules: from Python that took several times as long as their kernels.  `stream`: a torch stream of the
-# tensors' device (default: its current one); outputs and workspaces that are not given belong to it.
+# tensors' device (default: its current one); outputs and workspaces that are not given belong to it,
+# and, as with any torch stream, the inputs have to live until it has read them.
 
 _module = None
 
@@ -828,7 +829,7 @@ def zgcm_attn_decode_kv8(cache, q, g, pos, *, window=128, scale=None, blocks=Non
                          stream=None):
     """Decode attention of one token per sequence, the newest one appended: q [n_seq,Hq,D] (cache.key_dtype, prepared),
     g bf16 [n_seq,Hq,D] or None (no gate), pos int32 [n_seq].  blocks: int32 [n_seq,Hkv,n] from zgcm_kv8_select, the
-    earlier blocks to read (default: all that the window reaches).  workspace: a uint8 tensor of
+    earlier blocks to read, ascending (default: all that the window reaches).  workspace: a uint8 tensor of
     zgcm_attn_decode_kv8_workspace_size bytes.  Returns (out bf16 [n_seq,Hq,D], lse fp32 [n_seq,Hq])."""
     handle = _kv8(cache)
     return _done(_quick().attn_decode_kv8(*handle, q, g, pos, blocks, window, cache.D ** -0.5 if scale is None else scale, out,

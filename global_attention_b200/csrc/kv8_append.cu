@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(AP_THREADS, 4) kv8_append_kernel(const __grid_
 
 template <typename TK>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-    const dim3 grid((p.N + kBlk - 1) / kBlk + 1, p.c.Hkv, p.c.B);
+    const dim3 grid((p.N - 1) / kBlk + 2, p.c.Hkv, p.c.B);
     if (p.c.code == ZGCM_E4M3)
         kv8_append_kernel<TK, ZGCM_E4M3><<<grid, AP_THREADS, 0, stream>>>(p);
     else

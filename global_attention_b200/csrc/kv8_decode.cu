@@ -376,7 +376,7 @@ int plan(DecodeKv8Params& p, const zgcm_kv8_cache* cache, int Hq, int window, in
     p.HT = (p.G + DK_HEADS - 1) / DK_HEADS;
     p.rows = p.G < DK_HEADS ? p.G : DK_HEADS;
     p.W = window;
-    // items and their heads are counted in 32 bits (grids and records; 8 CTAs of an item)
+    // items and their heads are counted in 32 bits (grids and records)
     if ((long long)p.c.B * p.c.Hkv * p.HT * DK_HEADS > 0x7fffffffLL || n_list > 0x7ffffffe) return ZGCM_ERR_UNSUPPORTED;
     // the most units of an item: a list's entries, or the blocks that a window can touch and the table hold
     const long long touched = ((long long)window - 1 + kBlk - 1) / kBlk + 1;

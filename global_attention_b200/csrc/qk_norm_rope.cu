@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(QR_THREADS, 2) qk_norm_rope_bwd_kernel(const _
 }
 
 // dgamma[side][d] = sum over the CTAs' partials, in a fixed order: a CTA takes 32 of the 256 columns, each of its 32 warps
-// every 32nd partial, all of them on their way at once (8 warps, 4 loads at a time, took 5 us longer).
+// every 32nd partial, all of them on their way at once (with 8 warps and 4 loads at a time the
+// gradient of 1000 tokens took 16.5 us instead of 14.4).
 constexpr int QR_SUM_THREADS = 1024, QR_SUM_WARPS = QR_SUM_THREADS / 32;
 __global__ void __launch_bounds__(QR_SUM_THREADS) qk_dgamma_kernel(const float* part, int n, float* dgamma_q, float* dgamma_k) {
     constexpr int MOST = (QR_BWD_CTAS + QR_SUM_WARPS - 1) / QR_SUM_WARPS;

@@ -81,8 +81,8 @@ int zgcm_kv8_append(const zgcm_kv8_cache* cache, const void* k, long long k_b_st
  * with k_j, v_j of p's own block floor(p/64) as in the tail and of earlier blocks as their
  * codes stand for.  blocks (may be NULL): int32 [n_seq, Hkv, n_list], the earlier blocks to
  * read, ascending, for example from zgcm_kv8_select; an entry that is negative, not below p's own
- * block, wholly before the window or not above the entry before it is passed over.  The own
- * block is always read.
+ * block, wholly before the window or not above the entry before it is passed over.  (The entry directly before is
+ * all that is looked at: a list that is not ascending may bring a block in twice.)  The own block is always read.
  * q [n_seq, Hq, D] key_type; g [n_seq, Hq, D] bf16, or NULL for no gate (out = the softmax's
  * mean); out bf16 [n_seq, Hq, D]; lse fp32 [n_seq, Hq].  Idle sequences: out 0, lse -inf.
  * A window that reaches further back than n_blocks blocks (the own one among them): NaN.
