@@ -203,7 +203,8 @@ def _check_bwd(x, gamma, pos, dy, R, dx, dgamma, dtype):
 @pytest.mark.parametrize("T,Hq,Hkv,R,xt,yt", [
     (1, 32, 8, 42, "bf16", "bf16"), (1, 1, 1, 42, "bf16", "fp16"), (5, 3, 1, 128, "fp16", "fp16"),
     (67, 32, 8, 42, "bf16", "fp16"), (700, 5, 2, 0, "bf16", "bf16"), (595, 12, 1, 2, "fp32", "fp32"),
-    (1203, 16, 2, 42, "fp32", "bf16"), (2401, 4, 4, 64, "fp16", "fp32"), (130, 32, 8, 126, "fp16", "bf16"),
+    (1203, 16, 2, 42, "fp32", "bf16"), (2401, 4, 4, 64, "fp16", "fp32"), (130, 32, 8, 126, "fp16", "bf16"), (5003, 4, 2, 42, "bf16", "bf16"), (8001, 3, 1, 42, "fp16", "bf16"),
+    (7500, 1, 2, 40, "fp32", "fp32"),
 ])
 def test_against_oracle(cuda, T, Hq, Hkv, R, xt, yt):
     q, k, gq, gk, pos, dqr, dkr = _inputs(T, Hq, Hkv, xt, yt, seed=T)
@@ -296,6 +297,55 @@ def test_autograd_on_the_gpu(cuda):
 
 def qkrope_dgamma(q, gq, seq, dy):
     return torch.from_numpy(qkrope.backward(q, gq, seq, dy)[1])
+
+
+@gpu
+def test_autograd_shared_gamma_broadcast_input_and_capture(cuda):
+    """One gamma for q and k, one sequence's q broadcast over the batch; then forward and backward in a graph, replayed
+    on new inputs."""
+    q, k, g, _, _, dqr, dkr = _inputs(24, 4, 2, "fp32", "fp32", seed=3)
+    leaves = [q[:12].cuda().requires_grad_(), k.cuda().view(2, 12, 2, 128).requires_grad_(), g.cuda().requires_grad_()]
+    dy = [dqr.cuda().view(2, 12, 4, 128), dkr.cuda().view(2, 12, 2, 128)]
+
+    def step():
+        y = zgcm_qk_norm_rope(leaves[0].expand(2, 12, 4, 128), leaves[1], leaves[2], leaves[2])
+        return torch.autograd.grad(y, leaves, dy)
+
+    got = step()
+    seq = torch.arange(12, dtype=torch.int32).repeat(2)
+    both = q[:12].repeat(2, 1, 1)
+    dq, dgq = qkrope.backward(both, g, seq, dqr)
+    dk, dgk = qkrope.backward(k, g, seq, dkr)
+    # as in _check_bwd: 2^-18 of the magnitudes of each part, and one more rounding of their sum
+    for n, ref, x, d, out in (("dq", dq, both, dqr, got[0]), ("dk", dk, k, dkr, got[1])):
+        xd, dyd = np.abs(x.double().numpy()), np.abs(d.double().numpy())
+        rms = np.sqrt((xd * xd).mean(-1, keepdims=True) + 1e-6)
+        w = (dyd + _partner(dyd, 42)) * np.abs(g.double().numpy())
+        mag = w / rms + xd * (w * xd).mean(-1, keepdims=True) / rms ** 3
+        if n == "dq":
+            ref, mag = ref[:12] + ref[12:], mag[:12] + mag[12:]
+        _near(n, out.view(ref.shape), ref, mag, torch.float32, 2.0 ** -17)
+    xd = [np.abs(t.double().numpy()) for t in (both, k, dqr, dkr)]
+    mag = sum((x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * (d + _partner(d, 42))).sum((0, 1))
+              for x, d in ((xd[0], xd[2]), (xd[1], xd[3])))
+    err = np.abs(got[2].double().cpu().numpy() - dgq - dgk)
+    assert (err <= (2.0 ** -19 + 110 * 2.0 ** -24) * mag).all()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    with torch.no_grad():
+        leaves[0].mul_(0.5).add_(0.25)
+        dy[1].neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(held, step()):
+        assert torch.equal(x, y)
 
 
 @gpu
