@@ -9,12 +9,13 @@
 // need them: the tensor cores give every score in fp32 (16 blocks by 8 heads an instruction), off by less than
 //      eps = 2^-14.5 max_h |q_h|_1 max_j |k_mean_j|_max
 // (8 sums of 17 terms, each off by 2^-22 of the largest of them at most: 2^-14.9 of the terms' sum; the histogram's own
-// roundings are small against the rest); one histogram of 1024 or 4096 equal steps finds the step that holds the need-th highest of them, whose edges are v0 and v1; what lies above
-// v1 + 2 eps is taken, what lies below v0 - 2 eps is not, and the few between are scored in fp64 and ranked by
-// counting.  (All scores in fp64, on the fp64 matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for 32 of
-// up to 256 blocks of 64 x 8 items, or 64 of 4096 of 2 x 8, against 14.5 and 18.1 here.)  Where more than 256 are
-// between, many equal scores say, or a score is not finite, all are scored in fp64 and the histogram is taken of those (as ordered 64-bit integers), as often as one step
-// of it holds too many.
+// roundings are small against the rest).  One histogram of 1024 or 4096 equal steps finds the step that holds the need-th
+// highest of them, whose edges are v0 and v1; what lies above v1 + 2 eps is taken, what lies below v0 - 2 eps is not, and the
+// few between are scored in fp64 and ranked by counting, unless all of them are needed.  (All scores in fp64, on the fp64
+// matrix instruction, took 1.5 us for 8 blocks of a warp: 29 us for 32 of up to 256 blocks of 64 x 8 items, or 64 of 4096
+// of 2 x 8, against 14.5 and 18.1 here.)  Where more than 256 are between, many equal scores say, or a score is not finite,
+// all are scored in fp64 and the histogram is taken of those (as ordered 64-bit integers), as often as one step of it holds
+// too many.
 //
 // A cluster of CTAs takes one (sequence, KV head): each scores a slice of the blocks and writes the scores into
 // the first CTA's shared memory, which does the rest.  On a B200 the scoring of 64 x 8 items (26 MB of means) is 6 of the

@@ -2,7 +2,7 @@
 // the module global_attention_b200._calls, under the functions of the same names in __init__.py.
 //
 // A decode step is a handful of calls of a few microseconds each on the device.  Checking tensors and making
-// outputs from Python took 10 to 30 us a call, several times the kernels; here it takes 1 or 2.  The rules
+// outputs from Python took 10 to 30 us a call, several times the kernels; here it takes 1 to 3.  The rules
 // are those of the rest of the binding: every tensor's type, layout, shape and device is checked
 // before the library is called, a wrong one raises TypeError, a status of the library is returned as an int.
 #include <Python.h>
