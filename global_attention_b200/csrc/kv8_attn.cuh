@@ -156,8 +156,15 @@ __device__ __forceinline__ float quad_max(float x) {
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// A warp's share of an item.  Lane (r, c) = (lane / 4, lane % 4) holds the heads 2 c and 2 c + 1 (.x and .y): of O, for
+// A warp's share of an item.  Lane (r, c) = (lane / 4, lane % 4) holds the columns 2 c and 2 c + 1 (.x and .y): of O, for
 // i = 0 .. 7, the dims 16 i + 2 r in o[i][0] and 16 i + 2 r + 1 in o[i][1].
+//
+// Columns are heads.  p enters the second product in two halves, hi = fp16(p) and lo = fp16(p - hi), 22 bits of it (one half
+// alone is off by up to 2^-12 of each p: an output that cancels to 2^-12 of sum p |v| was lost).  WIDE items (more
+// than 4 heads in a group) multiply twice.  Others have the columns 4 .. 7 free: they hold the four heads again, the same
+// scores, maxima and sums, but take the low halves, and O's two columns of a head are added at the item's end: no
+// product more than with one half.  Measured with one half / with both (us): 64 sequences of up to 16K, INT8, 8 KV heads of 4
+// 273 / 280, 4 of 8 158 / 152, 2 of 16 137 / 143; 64 of up to 8K, one of 12 59 / 72; 32 listed blocks 24.6 / 24.6.
 struct State {
     float2 m, l;      // running maximum (base 2), this lane's part of the sum (times 2^14)
     float2 o[8][2];
@@ -173,7 +180,7 @@ __device__ __forceinline__ void join_o(State& t, int i, const float (&d)[4], flo
     t.o[i][1] = ffma2(make_float2(d[2], d[3]), f, fmul2(t.o[i][1], a));
 }
 
-// Scores of a set of keys in base 2 (N of this lane's two heads) -> p relative to the set's own maximum (times 2^14: as
+// Scores of a set of keys in base 2 (N of this lane's two columns) -> p relative to the set's own maximum (times 2^14: as
 // fp16 down to 2^-38 of it, whatever the sets before had), the running maximum and sum.  a: factor for O so far; b: for
 // this set's.
 template <int N> __device__ __forceinline__ void soften(State& t, float2 (&s)[N], float2& a, float2& b) {
@@ -229,9 +236,10 @@ __device__ __forceinline__ void scores32(float2 (&s)[4], const uint32_t (&q)[8][
     }
 }
 
-// O takes in 32 keys: b fragments of their p (two of each 16 keys), their values at v_addr.
-template <int CODE>
-__device__ __forceinline__ void values32(State& t, const uint32_t (&pb)[4], float2 a, float2 f, uint32_t v_addr) {
+// O takes in 32 keys: b fragments of their p (two of each 16 keys; WIDE: of the high halves, then of the low ones), their
+// values at v_addr.
+template <int CODE, bool WIDE>
+__device__ __forceinline__ void values32(State& t, const uint32_t (&pb)[WIDE ? 8 : 4], float2 a, float2 f, uint32_t v_addr) {
     const int lane = threadIdx.x & 31, mi = lane >> 3, r = lane & 7;
     // 16 dims at a time (their 16-byte chunk); matrices are groups of 8 keys, transposed: a lane gets keys
     // 2 c, 2 c + 1 of the dims 2 r, 2 r + 1 of the chunk (rows r and r + 8 of the product)
@@ -244,13 +252,17 @@ __device__ __forceinline__ void values32(State& t, const uint32_t (&pb)[4], floa
         for (int j = 0; j < 4; ++j) pairs_apart<CODE>(w[j], x[j], y[j]);
         mma16816<false>(d, x[0], y[0], x[1], y[1], pb[0], pb[1], 0.f, 0.f, 0.f, 0.f);
         mma16816<false>(d, x[2], y[2], x[3], y[3], pb[2], pb[3]);
+        if constexpr (WIDE) {
+            mma16816<false>(d, x[0], y[0], x[1], y[1], pb[4], pb[5]);
+            mma16816<false>(d, x[2], y[2], x[3], y[3], pb[6], pb[7]);
+        }
         join_o(t, i, d, a, f);
     }
 }
 
 // 16 keys of the tail, k0 .. k0 + 15 of its block, valid where first <= key <= last; 16-bit products of the
-// types as they are (values in bf16 span more than fp16 does, so p goes in as two bf16, 16 bits of it)
-template <typename TK> struct Tail {
+// types as they are (values in bf16 span more than fp16 does, so p goes in as three bf16, its 24 bits)
+template <typename TK, bool WIDE> struct Tail {
     uint2 kw[2][8];
     uint32_t vw[8][4];
     __device__ __forceinline__ void load(const DecodeKv8Params& p, size_t seq_head, int k0) {
@@ -270,8 +282,8 @@ template <typename TK> struct Tail {
     __device__ __forceinline__ void take(State& t, const uint32_t (&q)[8][2], float scale, int k0, int first, int last);
 };
 
-template <typename TK>
-__device__ __forceinline__ void Tail<TK>::take(State& t, const uint32_t (&q)[8][2], float scale, int k0, int first, int last) {
+template <typename TK, bool WIDE>
+__device__ __forceinline__ void Tail<TK, WIDE>::take(State& t, const uint32_t (&q)[8][2], float scale, int k0, int first, int last) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -296,26 +308,31 @@ __device__ __forceinline__ void Tail<TK>::take(State& t, const uint32_t (&q)[8][
     float2 a, b;
     soften(t, s, a, b);
     b = fmul2(b, make_float2(kInvP, kInvP));
-    uint32_t hi[2], lo[2];
+    uint32_t part[3][2];   // first to third part of p; not WIDE: the second in the upper columns of the first
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        hi[n] = pack_bf16(s[n].x, s[n].y);
-        const float2 x = unpack_bf16(hi[n]);
-        lo[n] = transpose8(pack_bf16(s[n].x - x.x, s[n].y - x.y));
-        hi[n] = transpose8(hi[n]);
+        const uint32_t hi = pack_bf16(s[n].x, s[n].y);
+        const float2 x = unpack_bf16(hi), left = make_float2(s[n].x - x.x, s[n].y - x.y);
+        const uint32_t mid = pack_bf16(left.x, left.y);
+        const float2 y = unpack_bf16(mid);
+        const uint32_t lo = pack_bf16(left.x - y.x, left.y - y.y);
+        part[0][n] = transpose8(WIDE || c < 2 ? hi : mid);
+        part[1][n] = transpose8(WIDE ? mid : c < 2 ? lo : 0u);
+        part[2][n] = WIDE ? transpose8(lo) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float e[4];
         const uint32_t a0 = __byte_perm(vw[i][0], vw[i][1], 0x5410), a1 = __byte_perm(vw[i][0], vw[i][1], 0x7632);
         const uint32_t a2 = __byte_perm(vw[i][2], vw[i][3], 0x5410), a3 = __byte_perm(vw[i][2], vw[i][3], 0x7632);
-        mma16816<true>(e, a0, a1, a2, a3, hi[0], hi[1], 0.f, 0.f, 0.f, 0.f);
-        mma16816<true>(e, a0, a1, a2, a3, lo[0], lo[1]);
+        mma16816<true>(e, a0, a1, a2, a3, part[0][0], part[0][1], 0.f, 0.f, 0.f, 0.f);
+        mma16816<true>(e, a0, a1, a2, a3, part[1][0], part[1][1]);
+        if (WIDE) mma16816<true>(e, a0, a1, a2, a3, part[2][0], part[2][1]);
         join_o(t, i, e, a, b);
     }
 }
 
-// Where a warp's maximum and sum go, [head]; every lane of the warp calls it.
+// Where a warp's maximum and sum go, [column]; every lane of the warp calls it.
 __device__ __forceinline__ void put_ml(const State& t, float (*ml)[2]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
     const float lx = column_sum(t.l.x), ly = column_sum(t.l.y);
@@ -325,7 +342,7 @@ __device__ __forceinline__ void put_ml(const State& t, float (*ml)[2]) {
     }
 }
 
-// The maximum and sum of four warps' parts of head h, and the factor of warp w's
+// The maximum and sum of four warps' parts of column h, and the factor of warp w's
 __device__ __forceinline__ float join_ml(const float (*ml)[DK_HEADS][2], int h, int w, float& m, float& l) {
     float f = 0.f;
     m = -INFINITY;
@@ -363,20 +380,20 @@ __device__ __forceinline__ void finish4(const DecodeKv8Params& p, size_t head, i
 }
 
 
-// This lane's 32 elements of its head's q (r < nh, zeros else): chunk i's pairs 16 i + 4 c, + 2
-template <typename TK>
-__device__ __forceinline__ void load_q(const DecodeKv8Params& p, size_t head, bool on, uint32_t (&q)[8][2]) {
-    const int c = threadIdx.x & 3;
+// This lane's 32 elements of its column's q (zeros past the nh heads; head: the item's first): chunk i's pairs 16 i + 4 c, + 2
+template <typename TK, bool WIDE>
+__device__ __forceinline__ void load_q(const DecodeKv8Params& p, size_t head, int nh, uint32_t (&q)[8][2]) {
+    const int c = threadIdx.x & 3, column = (threadIdx.x & 31) >> 2, h = WIDE ? column : column & 3;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint2 u = make_uint2(0u, 0u);
-        if (on) u = *reinterpret_cast<const uint2*>(static_cast<const TK*>(p.q) + head * kD + 16 * i + 4 * c);
+        if (h < nh) u = *reinterpret_cast<const uint2*>(static_cast<const TK*>(p.q) + (head + h) * kD + 16 * i + 4 * c);
         q[i][0] = u.x;
         q[i][1] = u.y;
     }
 }
 
-// q as the fp16 that meets codes, and the scales of the scores of this lane's two heads in base 2: fp16 as it is, bf16
+// q as the fp16 that meets codes, and the scales of the scores of this lane's two columns in base 2: fp16 as it is, bf16
 // times the power of two that brings the head's largest element to 2^14
 template <typename TK>
 __device__ __forceinline__ float2 q_as_half(const DecodeKv8Params& p, const uint32_t (&q)[8][2], uint32_t (&h)[8][2]) {
@@ -402,7 +419,7 @@ __device__ __forceinline__ float2 q_as_half(const DecodeKv8Params& p, const uint
         }
     }
     if (!KeyType<TK>::kBf) return make_float2(p.scale_log2, p.scale_log2);
-    const float qs = p.scale_log2 / up;   // of head r; this lane needs those of 2 c and 2 c + 1
+    const float qs = p.scale_log2 / up;   // of column r; this lane needs those of 2 c and 2 c + 1
     const int c = threadIdx.x & 3;
     return make_float2(__shfl_sync(0xffffffffu, qs, 8 * c), __shfl_sync(0xffffffffu, qs, 8 * c + 4));
 }
@@ -512,8 +529,8 @@ struct Stream {
         ok = __all_sync(0xffffffffu, ok);
         return ok;
     }
-    // Block n of `blocks`; qs: the scales of this lane's two heads' scores.  fetch(i): looks the 32 blocks from 32 i up.
-    template <int CODE, typename Fetch>
+    // Block n of `blocks`; qs: the scales of this lane's two columns' scores.  fetch(i): looks the 32 blocks from 32 i up.
+    template <int CODE, bool WIDE, typename Fetch>
     __device__ __forceinline__ void take(State& t, const uint32_t (&q)[8][2], float2 qs, int lo, int n, int blocks, int where,
                                          const Fetch& fetch) {
         const uint32_t base = smem_u32(ring);
@@ -526,16 +543,21 @@ struct Stream {
                            lo - k.j * kBlk - ((threadIdx.x >> 5) & 1) * kHalfKeys);
         reuse(2 * n + 3, 2 * blocks);
         float2 a, b;
-        uint32_t pb[4];
+        uint32_t pb[WIDE ? 8 : 4];
         if (on) {
             soften(t, s, a, b);
-            // p as fp16, 2^-11 of it off at most: an eighth of what the output's own rounding to bf16 is, before the
-            // sum over keys evens it out (the sum of p itself is fp32)
+            const bool upper = (threadIdx.x & 3) >= 2;   // columns 4 .. 7
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pb[i] = transpose8(pack_half(s[i].x, s[i].y));
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t hi = pack_half(s[i].x, s[i].y);
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                const uint32_t lo_half = pack_half(s[i].x - x.x, s[i].y - x.y);
+                pb[i] = transpose8(!WIDE && upper ? lo_half : hi);
+                if constexpr (WIDE) pb[4 + i] = transpose8(lo_half);
+            }
         }
         if (wait(2 * n + 1, where) && on)
-            values32<CODE>(t, pb, a, fmul2(b, make_float2(k.vs * kInvP, k.vs * kInvP)), base + (2 * n + 1) % kSlots * kSlot);
+            values32<CODE, WIDE>(t, pb, a, fmul2(b, make_float2(k.vs * kInvP, k.vs * kInvP)), base + (2 * n + 1) % kSlots * kSlot);
         if (n + 2 < blocks && ((n + 2) & 31) == 0) mine = fetch((n + 2) >> 5);
         reuse(2 * n + 4, 2 * blocks);
         if (n + 2 < blocks) note(n + 2);

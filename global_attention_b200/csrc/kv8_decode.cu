@@ -153,7 +153,7 @@ __device__ __forceinline__ int find_run(const DecodeKv8Params& p, DecodeSmem& sm
 
 __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <typename TK, int CODE>
+template <typename TK, int CODE, bool WIDE>
 __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_constant__ DecodeKv8Params p) {
     extern __shared__ unsigned char raw[];
     DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -194,18 +194,18 @@ __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_
         const bool has_tail = w.off + n == s.units;
         const int kvh = w.rest / p.HT, ht = w.rest % p.HT;
         const int nh = min(DK_HEADS, p.G - ht * DK_HEADS);
-        const size_t head = (size_t)w.b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS + r;   // this lane's head (r < nh)
+        const size_t head = (size_t)w.b * p.Hq + (size_t)kvh * p.G + ht * DK_HEADS;       // the item's first
         const bool one = w.off == 0 && has_tail;                               // the whole item
         if (s.idle || s.bad) {
-            if (warp == 0 && r < nh) no_answer(p, head, s.idle);
+            if (warp == 0 && r < nh) no_answer(p, head + r, s.idle);
         } else {
             State t;
             uint32_t qt[8][2], q16[8][2];   // as they are, for the tail; as fp16, for codes
-            load_q<TK>(p, head, r < nh, qt);
+            load_q<TK, WIDE>(p, head, nh, qt);
             if (has_tail) {
                 const int last = run.pos(w.b) - s.own * kBlk, first = s.lo - s.own * kBlk;
                 if (warp * 16 <= last && warp * 16 + 15 >= first) {
-                    Tail<TK> tail;
+                    Tail<TK, WIDE> tail;
                     tail.load(p, (size_t)w.b * p.c.Hkv + kvh, warp * 16);
                     tail.take(t, qt, p.scale_log2, warp * 16, first, last);
                 }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_
             for (int i = (team - slot) & 1; i < n8; i += 2) {
                 const int k = (slot + i) >> 1;
                 if (stream.ok) gave_up = k;
-                stream.take<CODE>(t, q16, qs, s.lo, k, blocks, DK_WAIT, fetch);
+                stream.take<CODE, WIDE>(t, q16, qs, s.lo, k, blocks, DK_WAIT, fetch);
             }
             // the four warps' parts, always added in the same order
             put_ml(t, sm.ml[warp]);
@@ -240,17 +240,21 @@ __global__ void __launch_bounds__(DK_THREADS, 4) kv8_decode_kernel(const __grid_
                 }
                 warps_sync();
             }
-            // 256 places of a head and 4 dims
+            // places of a head and 4 dims
             const size_t item = ((size_t)w.b * p.c.Hkv + kvh) * p.HT + ht;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < (WIDE ? 2 : 1); ++i) {
                 const int h = (tid + DK_THREADS * i) >> 5, d = 4 * (tid & 31);
                 if (h < nh) {
                     join_ml(sm.ml, h, 0, m, l);
-                    const float4 y = *reinterpret_cast<const float4*>(&sm.acc[h][d]);
+                    float4 y = *reinterpret_cast<const float4*>(&sm.acc[h][d]);
+                    if (!WIDE) {   // and what the low halves of p gave
+                        const float4 z = *reinterpret_cast<const float4*>(&sm.acc[h + DK_HEADS / 2][d]);
+                        y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+                    }
                     const float o[4] = {y.x, y.y, y.z, y.w};
                     if (one) {
-                        finish4(p, head - r + h, d, m, l, o, load_gate(p, head - r + h, d));
+                        finish4(p, head + h, d, m, l, o, load_gate(p, head + h, d));
                     } else {
                         float* rec = p.part + ((item + blockIdx.x) * p.rows + h) * DK_REC;
                         if (d == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
@@ -347,11 +351,12 @@ bool make_map(CUtensorMap* map, const void* codes, const Kv8& c) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
+template <typename TK, int CODE, bool WIDE> cudaError_t launch_kernels(const DecodeKv8Params& p, cudaStream_t stream) {
     const size_t smem = sizeof(DecodeSmem) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel = kv8_decode_kernel<TK, CODE, WIDE>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kv8_decode_kernel<TK, CODE><<<DK_CTAS, DK_THREADS, smem, stream>>>(p);
+    kernel<<<DK_CTAS, DK_THREADS, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * p.HT * p.rows));
@@ -363,6 +368,10 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kv8_join_kernel, p);
+}
+
+template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
+    return p.G > DK_HEADS / 2 ? launch_kernels<TK, CODE, true>(p, stream) : launch_kernels<TK, CODE, false>(p, stream);
 }
 
 // Checks and the shape-dependent part of the parameters; n_list < 0: no list.

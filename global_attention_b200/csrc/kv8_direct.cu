@@ -31,7 +31,7 @@ struct DirectSmem {
     WarpSmem warp[4];
     float ml[4][DK_HEADS][2];
     float from_ml[DD_SPLIT][DK_HEADS][2];      // [CTA of the cluster]: its maximum and sum
-    float4 from[256];                   // [CTA][place of this CTA's share]: its O
+    float4 from[2 * DD_THREADS];               // [CTA][place of this CTA's share]: its O
     int abort;
 };
 
@@ -42,7 +42,7 @@ __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("pre
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-template <typename TK, int CODE>
+template <typename TK, int CODE, bool WIDE>
 __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_constant__ DecodeKv8Params p) {
     extern __shared__ unsigned char raw[];
     __shared__ DirectSmem sm;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     if (warp == 3 && p.c.NB <= 2048)
         for (int i = lane; i < (p.c.NB * 4 + 127) / 128; i += 32) prefetch_line(p.c.table + (size_t)b * p.c.NB + min(32 * i, p.c.NB - 1));
     uint32_t qt[8][2];
-    load_q<TK>(p, head0 + r, r < nh, qt);
+    load_q<TK, WIDE>(p, head0, nh, qt);
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&sm.warp[warp].full[i], 1);
         if (warp == 0) sm.abort = 0;
@@ -78,11 +78,12 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
         if (p.split > 1) cluster_wait();
         return;
     }
-    // this thread's places, of a head and 4 dims each: of 256, or of the CTA's share of them
-    const int share = 256 / p.split;
-    uint2 gate[2];
+    // this thread's places, of a head and 4 dims each: of all, or of the CTA's share of them
+    constexpr int EACH = WIDE ? 2 : 1, PLACES = EACH * DD_THREADS;
+    const int share = PLACES / p.split;
+    uint2 gate[EACH];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < EACH; ++i) {
         const int at = rank * share + tid + DD_THREADS * i, h = at >> 5;
         gate[i] = tid + DD_THREADS * i < share && h < nh ? load_gate(p, head0 + h, 4 * (at & 31)) : make_uint2(0u, 0u);
     }
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     if (rank == 0) {   // while the first codes are on their way
         const int last = pos - s.own * kBlk, first = s.lo - s.own * kBlk;
         if (warp * 16 <= last && warp * 16 + 15 >= first) {
-            Tail<TK> tail;
+            Tail<TK, WIDE> tail;
             tail.load(p, seq_head, warp * 16);
             tail.take(t, qt, p.scale_log2, warp * 16, first, last);
         }
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     int gave_up = 0;
     for (int k = 0; k < nt; ++k) {
         if (stream.ok) gave_up = k;
-        stream.take<CODE>(t, q16, qs, s.lo, k, nt, DD_WAIT, fetch);
+        stream.take<CODE, WIDE>(t, q16, qs, s.lo, k, nt, DD_WAIT, fetch);
     }
     stream.drain(gave_up, nt);
     // the warps' parts, in a fixed order; the ring is free once all have come here
@@ -130,12 +131,12 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     __syncthreads();
     if (p.split > 1) cluster_wait();   // every CTA of the cluster runs
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < EACH; ++i) {
         const int at = tid + DD_THREADS * i, h = at >> 5, d = 4 * (at & 31);
         float4 x = *reinterpret_cast<const float4*>(&acc[0][h][d]);
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(&acc[w][h][d]);
+        for (int w = 1; w < (WIDE ? 4 : 8); ++w) {   // the warps' columns h, then what the low halves of p gave
+            const float4 y = *reinterpret_cast<const float4*>(&acc[w & 3][h + (w >> 2) * (DK_HEADS / 2)][d]);
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
         if (p.split == 1) {
@@ -181,11 +182,12 @@ __global__ void __launch_bounds__(DD_THREADS, 4) kv8_direct_kernel(const __grid_
     if (tid == 0 && sm.abort) *p.err = sm.abort;
 }
 
-template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
+template <typename TK, int CODE, bool WIDE> cudaError_t launch_kernel(const DecodeKv8Params& p, cudaStream_t stream) {
     const size_t smem = DD_RING + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel = kv8_direct_kernel<TK, CODE, WIDE>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    if (p.split > 8) e = cudaFuncSetAttribute(kv8_direct_kernel<TK, CODE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (p.split > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.c.B * p.c.Hkv * p.HT * p.split));
@@ -198,7 +200,11 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_direct_kernel<TK, CODE>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cudaStream_t stream) {
+    return p.G > DK_HEADS / 2 ? launch_kernel<TK, CODE, true>(p, stream) : launch_kernel<TK, CODE, false>(p, stream);
 }
 
 }  // namespace

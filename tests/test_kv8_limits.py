@@ -1,0 +1,44 @@
+"""The 8-bit block cache (include/zgcm_kv8.h) where its arithmetic and its calls are strained.  Against the
+oracle of the definition, as tests/test_kv8.py, whose helpers these tests use; tolerances beyond those of that file are
+derived at each test.
+"""
+import numpy as np
+import pytest
+import torch
+
+import global_attention_b200 as ga
+from oracle import kv8
+from test_kv8 import ALL, KEY, _feed, _i32, _new, cuda  # noqa: F401  (cuda: the fixture)
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+@pytest.mark.parametrize("code,key", [("e4m3", "bf16"), ("int8", "fp16")])
+@pytest.mark.parametrize("Hq,Hkv,S", [(4, 1, 64), (3, 1, 40), (8, 1, 64), (4, 4, 320), (32, 8, 320), (8, 1, 320), (12, 1, 640),
+                                      (4, 1, 33280), (12, 1, 33280)])
+def test_outputs_that_cancel(cuda, code, key, Hq, Hkv, S):  # noqa: F811
+    """Every other token's score is d higher and its value the other's negative: out = -v tanh(d / 2), a 2^-11th of
+    sum p |v| and less, which probabilities of 11 or 16 bits do not give.
+
+    Bound relative to sum p |v|, with p exact to 2^-22 (exp2; its two fp16 halves, or three bf16 parts in the newest
+    block): sums on the tensor cores, 2^-23 a step, of a block's 32 keys and 16-key steps, 4 warps and 16 CTAs: within
+    2^-19 for the newest block alone, within 2^-17 for the sums of many blocks.  An error of the normaliser is
+    one of out itself: 2^-17 of it.  Scores are at most d, their errors 2^-16 d: e below 2^-25."""
+    g = torch.Generator().manual_seed(S + Hq)
+    k = torch.zeros(1, S, Hkv, 128)
+    k[:, 1::2, :, 0] = 1.0
+    v = torch.randn(1, 1, Hkv, 128, generator=g).repeat(1, S, 1, 1)
+    v[:, 1::2] *= -1
+    d = 2.0 ** (-14 + 4 * torch.rand(Hq, generator=g))
+    q = torch.zeros(1, Hq, 128)
+    q[0, :, 0] = d * 128 ** 0.5
+    k, v, q = k.to(KEY[key]), v.to(torch.bfloat16), q.to(KEY[key])
+    c = _new(1, -(-S // 64), Hkv, code, key)
+    _feed(c, k, v, [S])
+    out, lse = ga.zgcm_attn_decode_kv8(c, q.cuda(), None, _i32(S - 1), window=ALL)
+    ref, ref_lse, mag, _ = kv8.attend(q[0], None, k[0], v[0], code=code, window=ALL)
+    assert (np.abs(ref) <= 2.0 ** -10.9 * mag).all()
+    err = np.abs(out[0].double().cpu().numpy() - ref) / (2.0 ** -8 * 1.001 * np.abs(ref) + 2.0 ** (-19 if S <= 64 else -17) * mag)
+    assert err.max() <= 1, float(err.max())
+    assert (np.abs(lse[0].double().cpu().numpy() - ref_lse) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(ref_lse)).all()
