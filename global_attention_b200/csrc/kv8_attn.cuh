@@ -192,11 +192,13 @@ template <int N> __device__ __forceinline__ void soften(State& t, float2 (&s)[N]
     const float2 m = make_float2(fmaxf(t.m.x, mt.x), fmaxf(t.m.y, mt.y));
     a = make_float2(fast_exp2(t.m.x - m.x), fast_exp2(t.m.y - m.y));   // 0 from the empty start
     b = make_float2(fast_exp2(mt.x - m.x), fast_exp2(mt.y - m.y));
-    const float2 base = make_float2(14.f - mt.x, 14.f - mt.y);
+    // the difference first, which is 0 for the largest: 14 - mt is rounded at mt's magnitude, so that from |mt| = 2^25 on p
+    // could come out as 2^16, past fp16
+    const float2 minus = make_float2(-mt.x, -mt.y), up = make_float2(14.f, 14.f);
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        s[i] = fadd2(s[i], base);
+        s[i] = fadd2(fadd2(s[i], minus), up);
         s[i] = make_float2(fast_exp2(s[i].x), fast_exp2(s[i].y));
         sum = fadd2(sum, s[i]);
     }
@@ -376,7 +378,7 @@ __device__ __forceinline__ void finish4(const DecodeKv8Params& p, size_t head, i
         x[3] *= sigmoidf_(b.y);
     }
     *reinterpret_cast<uint2*>(p.out + head * kD + d) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    if (d == 0) p.lse[head] = (m + log2f(l) - 14.f) * kLn2;
+    if (d == 0) p.lse[head] = (m + (log2f(l) - 14.f)) * kLn2;
 }
 
 

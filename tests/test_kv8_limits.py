@@ -42,3 +42,33 @@ def test_outputs_that_cancel(cuda, code, key, Hq, Hkv, S):  # noqa: F811
     err = np.abs(out[0].double().cpu().numpy() - ref) / (2.0 ** -8 * 1.001 * np.abs(ref) + 2.0 ** (-19 if S <= 64 else -17) * mag)
     assert err.max() <= 1, float(err.max())
     assert (np.abs(lse[0].double().cpu().numpy() - ref_lse) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(ref_lse)).all()
+
+
+@gpu
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("key", ["bf16", "fp16"])
+@pytest.mark.parametrize("S", [400, 33400])
+def test_scores_beyond_2_25(cuda, code, key, S):  # noqa: F811
+    """Finite keys and queries whose scores pass 2^25 in base 2, where fp32 counts in steps of 4 and more: one key takes
+    all, and out is its value as its code stands for it (p is exactly 1: one rounding to bf16, and 2^-20 for the scale and
+    the normaliser), lse its score (128 products in fp32: 2^-17, and 2^-22 for scale, base and rounding)."""
+    heads, at = 16, [5, 64 + 17, 300, 310]
+    g = torch.Generator().manual_seed(S)
+    k = torch.full((1, S, 4, 128), -2000.0)
+    v = torch.randn(1, S, 4, 128, generator=g).to(torch.bfloat16)
+    for h, t in enumerate(at):
+        k[0, t, h] = 2000.0
+    k = k.to(KEY[key])
+    amp = 2.0 ** torch.linspace(25.01, 28, heads) / (128 * 2000.0 * 128 ** -0.5 * np.log2(np.e))
+    q = amp.view(1, heads, 1).expand(1, heads, 128).contiguous().to(KEY[key])
+    c = _new(1, S // 64 + 1, 4, code, key)
+    _feed(c, k, v, [S])
+    out, lse = ga.zgcm_attn_decode_kv8(c, q.cuda(), None, _i32(S - 1), window=ALL)
+    held_k, held_v = kv8.stored(k[0], code), kv8.stored(v[0], code)
+    for h in range(heads):
+        t = at[h // 4]
+        s = (held_k[t, h // 4] * q[0, h].double().numpy()).sum() * 128 ** -0.5
+        assert s * np.log2(np.e) > 2.0 ** 25
+        ref, got = held_v[t, h // 4], out[0, h].double().cpu().numpy()
+        assert (np.abs(got - ref) <= (2.0 ** -8 * 1.001 + 2.0 ** -20) * np.abs(ref)).all(), (h, got[:4], ref[:4])
+        assert abs(float(lse[0, h]) - s) <= (2.0 ** -17 + 2.0 ** -22) * s
