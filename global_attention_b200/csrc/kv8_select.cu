@@ -474,16 +474,17 @@ template <typename TK, int THREADS> cudaError_t launch(const SelectParams& p, cu
     // 14.5, 21.2)
     int cs = 1;
     while (cs < 8 && items * cs < 148 && p.c.NB / (2 * cs) >= THREADS / 4) cs *= 2;
-    const int most = p.c.NB < kKv8MaxBlocks ? p.c.NB : kKv8MaxBlocks;
-    const size_t smem = sizeof(SelSmem) + (4u << kSelBits<THREADS>) + (size_t)most * 8;
+    constexpr size_t fixed = sizeof(SelSmem) + (4u << kSelBits<THREADS>), most = fixed + (size_t)kKv8MaxBlocks * 8;
     if (items * cs > 0x7fffffffLL) return cudaErrorInvalidValue;
     auto kernel = kv8_select_kernel<TK, THREADS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same limit in every call, whatever this one needs: the attribute is the kernel's, and a call on another thread may
+    // set it between here and the launch
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * cs));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = fixed + (size_t)p.c.NB * 8;   // NB <= kKv8MaxBlocks: checked
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -2,13 +2,16 @@
 oracle of the definition, as tests/test_kv8.py, whose helpers these tests use; tolerances beyond those of that file are
 derived at each test.
 """
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import global_attention_b200 as ga
 from oracle import kv8
-from test_kv8 import ALL, KEY, _feed, _i32, _new, cuda  # noqa: F401  (cuda: the fixture)
+from test_kv8 import ALL, KEY, _feed, _i32, _means, _new, _queries, cuda  # noqa: F401  (cuda: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -72,3 +75,35 @@ def test_scores_beyond_2_25(cuda, code, key, S):  # noqa: F811
         ref, got = held_v[t, h // 4], out[0, h].double().cpu().numpy()
         assert (np.abs(got - ref) <= (2.0 ** -8 * 1.001 + 2.0 ** -20) * np.abs(ref)).all(), (h, got[:4], ref[:4])
         assert abs(float(lse[0, h]) - s) <= (2.0 ** -17 + 2.0 ** -22) * s
+
+
+@gpu
+def test_select_from_two_threads(cuda):  # noqa: F811
+    """Contexts of different sizes from two threads at once, each on its own stream: no call may depend on what another one
+    has set for the kernel they share."""
+    jobs = []
+    for blocks in (1100, 16384):
+        c = _new(1, blocks, 1, "e4m3", "bf16", garbage=False)
+        _means(c, seed=blocks)
+        q, pos = _queries(1, 4, "bf16")[0].cuda(), _i32(64 * blocks - 1)
+        ref = ga.zgcm_kv8_select(c, q, pos, 8, window=ALL)
+        jobs.append((c, q, pos, ref, torch.empty_like(ref), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    lib, got = ga.load(), [set(), set()]
+
+    def work(i):
+        c, q, pos, _, out, stream = jobs[i]
+        q, pos, out = (ctypes.c_void_p(t.data_ptr()) for t in (q, pos, out))
+        for _ in range(3000):
+            got[i].add(lib.zgcm_kv8_select(ctypes.byref(c._c), q, pos, 4, 2 ** 31 - 1, 8, 1, 1, out,
+                                           ctypes.c_void_p(stream.cuda_stream)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert got == [{0}, {0}]
+    for _, _, _, ref, out, _ in jobs:
+        assert torch.equal(ref, out)
