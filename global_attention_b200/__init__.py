@@ -674,7 +674,9 @@ def zgcm_proj_out_bwd(a, w_o, dy, *, da=None, dw=None, stream=None):
 # The calls of a decode step check their tensors in csrc/torch_calls.cpp (the module _calls), by the
 # same rules: from Python that took several times as long as their kernels.  `stream`: a torch stream of the
 # tensors' device (default: its current one); outputs and workspaces that are not given belong to it,
-# and, as with any torch stream, the inputs have to live until it has read them.
+# and, as with any torch stream, the inputs have to live until it has read them.  Positions, counts and block lists
+# may be slices of longer tensors (one that does not begin at 16 bytes, as the library asks, is copied there first, on the
+# call's stream); the other tensors begin at 16 bytes.
 
 _module = None
 

@@ -101,6 +101,17 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype) {
                                      dtype, std::nullopt);
 }
 
+bool off(const Tensor& t) { return (reinterpret_cast<uintptr_t>(t.const_data_ptr()) & 15u) != 0; }
+
+// int32 positions, counts and lists may begin anywhere (a slice of a longer tensor), the library wants them at 16 bytes: others
+// are copied, on the stream of the call (`Here` lives), into `copy`
+const int* ints(const Tensor& t, Tensor& copy) {
+    if (!off(t)) return t.const_data_ptr<int>();
+    copy = fresh(t.sizes(), at::kInt);
+    copy.copy_(t);
+    return copy.const_data_ptr<int>();
+}
+
 int to_int(PyObject* o) {   // as the C int the library takes; larger ones are the largest
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -184,7 +195,7 @@ struct Qk {
     int x_type, index;
     zgcm_rows rq, rk;
     const float *gamma_q, *gamma_k;
-    const int* pos;
+    const Tensor& pos;
 };
 
 Qk qk_inputs(PyObject* const* a) {   // q, k, gamma_q, gamma_k, pos
@@ -202,8 +213,7 @@ Qk qk_inputs(PyObject* const* a) {   // q, k, gamma_q, gamma_k, pos
     on_device(gq, "gamma_q", index);
     on_device(gk, "gamma_k", index);
     on_device(pos, "pos", index);
-    return Qk{q, k, T, Hq, Hkv, D, dtype, x_type, index, rq, rk, gq.const_data_ptr<float>(), gk.const_data_ptr<float>(),
-              pos.const_data_ptr<int>()};
+    return Qk{q, k, T, Hq, Hkv, D, dtype, x_type, index, rq, rk, gq.const_data_ptr<float>(), gk.const_data_ptr<float>(), pos};
 }
 
 // (q, k, gamma_q, gamma_k, pos, rope_dims, rope_base, eps, out_dtype, qr, kr, stream)
@@ -229,8 +239,9 @@ PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor kr = given(a[10]) ? THPVariable_Unpack(a[10]) : fresh({x.T, x.Hkv, x.D}, out);
         on_device(qr, "qr", x.index);
         on_device(kr, "kr", x.index);
-        const int st = zgcm_qk_norm_rope_fwd(x.rq, x.rk, x.gamma_q, x.gamma_k, x.pos, (int)x.T, (int)x.Hq, (int)x.Hkv, (int)x.D,
-                                             x.x_type, y_type, to_int(a[5]), to_double(a[6]), (float)to_double(a[7]),
+        Tensor copy;
+        const int st = zgcm_qk_norm_rope_fwd(x.rq, x.rk, x.gamma_q, x.gamma_k, ints(x.pos, copy), (int)x.T, (int)x.Hq, (int)x.Hkv,
+                                             (int)x.D, x.x_type, y_type, to_int(a[5]), to_double(a[6]), (float)to_double(a[7]),
                                              rows(qr, "qr", out, {x.T, x.Hq, x.D}), rows(kr, "kr", out, {x.T, x.Hkv, x.D}),
                                              here.handle());
         return st == ZGCM_OK ? pair(qr, kr) : status(st);
@@ -271,8 +282,9 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t need = (int64_t)zgcm_qk_norm_rope_bwd_workspace_size((int)x.T);
         const Tensor ws = given(a[14]) ? THPVariable_Unpack(a[14]) : fresh({need}, at::kByte);
         on_device(ws, "workspace", x.index);
-        const int st = zgcm_qk_norm_rope_bwd(x.rq, x.rk, x.gamma_q, x.gamma_k, x.pos, rdqr, rdkr, (int)x.T, (int)x.Hq, (int)x.Hkv,
-                                             (int)x.D, x.x_type, y_type, to_int(a[7]), to_double(a[8]), (float)to_double(a[9]),
+        Tensor copy;
+        const int st = zgcm_qk_norm_rope_bwd(x.rq, x.rk, x.gamma_q, x.gamma_k, ints(x.pos, copy), rdqr, rdkr, (int)x.T, (int)x.Hq,
+                                             (int)x.Hkv, (int)x.D, x.x_type, y_type, to_int(a[7]), to_double(a[8]), (float)to_double(a[9]),
                                              rows(g[0], "dq", x.dtype, {x.T, x.Hq, x.D}),
                                              rows(g[1], "dk", x.dtype, {x.T, x.Hkv, x.D}), g[2].data_ptr<float>(),
                                              g[3].data_ptr<float>(), ws.data_ptr(), (size_t)ws.numel(), here.handle());
@@ -315,11 +327,11 @@ const Tensor& tokens(PyObject* o, const char* name, const Cache& c, at::ScalarTy
     return t;
 }
 
-const void* optional(PyObject* o, const char* name, at::ScalarType dtype, at::IntArrayRef shape, int index) {
+const Tensor* optional(PyObject* o, const char* name, at::ScalarType dtype, at::IntArrayRef shape, int index) {
     if (!given(o)) return nullptr;
     const Tensor& t = dense(o, name, dtype, shape);
     on_device(t, name, index);
-    return t.const_data_ptr();
+    return &t;
 }
 
 // (cache address, tensor of it, k, v, pos, count, stream)
@@ -332,11 +344,13 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor &k = tokens(a[2], "k", c, c.key, N, ks), &v = tokens(a[3], "v", c, at::kBFloat16, N, vs);
         const Tensor& pos = dense(a[4], "pos", at::kInt, {c.c->n_seq});
         on_device(pos, "pos", c.index);
-        const void* count = optional(a[5], "count", at::kInt, {c.c->n_seq}, c.index);
+        const Tensor* count = optional(a[5], "count", at::kInt, {c.c->n_seq}, c.index);
         const Here here(a[6], c.index);
-        return status(zgcm_kv8_append(c.c, k.const_data_ptr(), ks[0], ks[1], ks[2], v.const_data_ptr(), vs[0], vs[1], vs[2],
-                                      pos.const_data_ptr<int>(), static_cast<const int*>(count),
-                                      as_int(N, "the number of tokens"), here.handle()));
+        Tensor copies[2];
+        const int* at = ints(pos, copies[0]);
+        return status(zgcm_kv8_append(c.c, k.const_data_ptr(), ks[0], ks[1], ks[2], v.const_data_ptr(), vs[0], vs[1], vs[2], at,
+                                      count ? ints(*count, copies[1]) : nullptr, as_int(N, "the number of tokens"),
+                                      here.handle()));
     });
 }
 
@@ -351,9 +365,8 @@ PyObject* attn_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int n_list = given(a[5]) ? as_int(tensor(a[5], "blocks", 3).size(2), "the list") : -1;
         on_device(q, "q", c.index);
         on_device(pos, "pos", c.index);
-        const void* g = optional(a[3], "g", at::kBFloat16, {B, Hq, D}, c.index);
-        const void* blocks = optional(a[5], "blocks", at::kInt, {B, c.c->Hkv, n_list}, c.index);
-        if (n_list == 0) blocks = pos.const_data_ptr();   // an empty list is not read: only that there is one counts
+        const Tensor* g = optional(a[3], "g", at::kBFloat16, {B, Hq, D}, c.index);
+        const Tensor* list = optional(a[5], "blocks", at::kInt, {B, c.c->Hkv, n_list}, c.index);
         optional(a[8], "out", at::kBFloat16, {B, Hq, D}, c.index);
         optional(a[9], "lse", at::kFloat, {B, Hq}, c.index);
         if (given(a[10])) optional(a[10], "workspace", at::kByte, {tensor(a[10], "workspace", 1).numel()}, c.index);
@@ -372,7 +385,11 @@ PyObject* attn_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             mine = fresh({(int64_t)bytes}, at::kByte);
             ws = mine.data_ptr();
         }
-        const int st = zgcm_attn_decode_kv8(c.c, q.const_data_ptr(), g, pos.const_data_ptr<int>(), static_cast<const int*>(blocks),
+        Tensor copies[2];
+        const int* at = ints(pos, copies[0]);
+        // an empty list is not read: only that there is one counts
+        const int* blocks = !list ? nullptr : n_list == 0 ? at : ints(*list, copies[1]);
+        const int st = zgcm_attn_decode_kv8(c.c, q.const_data_ptr(), g ? g->const_data_ptr() : nullptr, at, blocks,
                                             n_list < 0 ? 0 : n_list, heads, window, (float)to_double(a[7]),
                                             out.data_ptr(), lse.data_ptr<float>(), ws, bytes, here.handle());
         return st == ZGCM_OK ? pair(out, lse) : status(st);
@@ -394,9 +411,13 @@ PyObject* kv8_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         optional(a[8], "out", at::kInt, shape, c.index);
         const Here here(a[9], c.index);
         const Tensor out = given(a[8]) ? THPVariable_Unpack(a[8]) : fresh(shape, at::kInt);
-        const int st = zgcm_kv8_select(c.c, q.const_data_ptr(), pos.const_data_ptr<int>(), as_int(Hq, "the number of heads"),
-                                       to_int(a[7]), n_select, to_int(a[5]), to_int(a[6]), out.data_ptr<int>(), here.handle());
-        return st == ZGCM_OK ? THPVariable_Wrap(out) : status(st);
+        const Tensor made = off(out) ? fresh(shape, at::kInt) : out;
+        Tensor copy;
+        const int st = zgcm_kv8_select(c.c, q.const_data_ptr(), ints(pos, copy), as_int(Hq, "the number of heads"), to_int(a[7]),
+                                       n_select, to_int(a[5]), to_int(a[6]), made.data_ptr<int>(), here.handle());
+        if (st != ZGCM_OK) return status(st);
+        if (!made.is_same(out)) out.copy_(made);
+        return THPVariable_Wrap(out);
     });
 }
 

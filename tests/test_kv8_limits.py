@@ -11,7 +11,7 @@ import torch
 
 import global_attention_b200 as ga
 from oracle import kv8
-from test_kv8 import ALL, KEY, _feed, _i32, _means, _new, _queries, cuda  # noqa: F401  (cuda: the fixture)
+from test_kv8 import ALL, KEY, _feed, _i32, _means, _new, _queries, _tokens, cuda  # noqa: F401  (cuda: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -107,3 +107,37 @@ def test_select_from_two_threads(cuda):  # noqa: F811
     assert got == [{0}, {0}]
     for _, _, _, ref, out, _ in jobs:
         assert torch.equal(ref, out)
+
+
+@gpu
+def test_slices_of_positions_and_lists(cuda):  # noqa: F811
+    """Positions, counts and lists as rows of longer tensors, 4, 8 and 12 bytes past a 16-byte boundary: the same bits as
+    tensors of their own, eagerly and in a graph that follows what is written into them; select's out in place."""
+    k, v = _tokens(3, 300, 2, "bf16", seed=31)
+    q, g = (x.cuda() for x in _queries(3, 4, "bf16"))
+    steps = _i32(*[-9] * 3, 0, 0, 0, 299, 280, 299, 299, 299, 299).view(4, 3)
+    count = _i32(-9, 300, 281, 300, -9)
+    kept = []
+    for cut in (lambda t: t, torch.clone):
+        c = _new(3, 5, 2, "e4m3", "bf16")
+        start, pos, n = cut(steps[1]), cut(steps[2]), cut(count[1:4])
+        assert cut is torch.clone or all(x.data_ptr() % 16 for x in (start, pos, n))
+        ga.zgcm_kv8_append(c, k.cuda(), v.cuda(), start, count=n)
+        lists = torch.full((20,), -9, dtype=torch.int32, device="cuda")
+        sel = ga.zgcm_kv8_select(c, q, pos, 3, window=ALL, out=lists[1:19].view(3, 2, 3) if cut is not torch.clone else None)
+        if cut is not torch.clone:
+            assert sel.data_ptr() == lists.data_ptr() + 4 and lists[0] == lists[-1] == -9
+        out = ga.zgcm_attn_decode_kv8(c, q, g, pos, window=ALL, blocks=sel)
+        kept.append([sel, *out, c.k_tail.nan_to_num(7.0), c.v_tail.nan_to_num(7.0), c.k_codes.view(torch.uint8)])
+        if cut is not torch.clone:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                held = ga.zgcm_attn_decode_kv8(c, q, g, pos, window=ALL)
+            for p in (299, 290):
+                steps[2] = p
+                graph.replay()
+                alone = ga.zgcm_attn_decode_kv8(c, q, g, _i32(p, p, p), window=ALL)
+                # (as bits: sequence 1 holds 281 tokens, what it reads past them is NaN on both sides)
+                assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(held, alone))
+            steps[2] = _i32(299, 280, 299)
+    assert all(torch.equal(x, y) for x, y in zip(*kept))
