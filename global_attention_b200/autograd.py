@@ -20,6 +20,13 @@ import math
 import torch
 
 
+def _placed(grad):
+    """A gradient as the kernels take it: an expanded one (of a sum, say) has rows that are not contiguous, a part of a larger
+    one (of a concatenation) need not begin at 16 bytes."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def _default_ops():
     import global_attention_b200 as ga
     return ga.zgcm_attn_fwd, ga.zgcm_attn_bwd, ga.zgcm_attn_saved_size
@@ -48,7 +55,7 @@ class ZgcmAttentionFunction(torch.autograd.Function):
     def backward(ctx, dout, _dlse):
         q, k, v, g, gamma_q, gamma_k, out, lse, store = ctx.saved_tensors
         extra = dict(saved=store) if ctx.has_store else {}
-        gr = ctx.bwd(q, k, v, g, gamma_q, gamma_k, out, lse, dout.contiguous(), **ctx.kw, **extra)
+        gr = ctx.bwd(q, k, v, g, gamma_q, gamma_k, out, lse, _placed(dout), **ctx.kw, **extra)
         return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dgamma_q"], gr["dgamma_k"],
                 None, None, None, None, None, None)
 
@@ -80,8 +87,7 @@ class ZgcmQkNormRopeFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dqr, dkr):
         q, k, gamma_q, gamma_k, pos = ctx.saved_tensors
-        # an expanded gradient (of a sum, say) has rows that are not contiguous
-        gr = ctx.ops[1](q, k, gamma_q, gamma_k, pos, dqr.contiguous(), dkr.contiguous(), **ctx.kw)
+        gr = ctx.ops[1](q, k, gamma_q, gamma_k, pos, _placed(dqr), _placed(dkr), **ctx.kw)
         return gr["dq"], gr["dk"], gr["dgamma_q"], gr["dgamma_k"], None, None, None, None, None, None
 
 
