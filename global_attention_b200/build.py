@@ -3,8 +3,10 @@
     python -m global_attention_b200.build [--verbose]
 
 Each csrc/*.cu is compiled by nvcc for sm_100a (objects under _build/), then linked into
-one shared library with the CUDA runtime linked statically.  csrc/torch_calls.cpp, the binding's
-quick calls, becomes the extension module global_attention_b200/_calls.so against it and torch.
+one shared library with the CUDA runtime linked statically: nvcc is all it takes.  Where torch is installed,
+csrc/torch_calls.cpp, the binding's quick calls, becomes the extension module global_attention_b200/_calls.so against the
+library and torch (g++, torch's and Python's headers); it is built again when torch or Python is another one.  Where it
+cannot be built the reason is printed, the library stands, and the calls that need the module raise.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libzgcm_attn.so")
 CALLS = os.path.join(HERE, "_calls.so")
+CALLS_FOR = os.path.join(OBJ, "_calls.for")   # the torch and the Python it was built for
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -62,15 +65,26 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
-    build_calls(force)
+    try:
+        build_calls(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write(f"{CALLS} is not built, the calls that need it will raise: {e}\n")
     return LIB
 
 
 def build_calls(force: bool = False) -> str:
     """The extension module of csrc/torch_calls.cpp (host code; the library beside it is found by $ORIGIN)."""
+    import torch
     src = os.path.join(CSRC, "torch_calls.cpp")
-    if force or _needs(CALLS, [src, __file__, *glob.glob(os.path.join(ROOT, "include", "*.h"))]):
-        import torch
+    wanted = f"torch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+    there = ""
+    if os.path.exists(CALLS_FOR):
+        with open(CALLS_FOR) as f:
+            there = f.read()
+    if force or there != wanted or _needs(CALLS, [src, __file__, *glob.glob(os.path.join(ROOT, "include", "*.h"))]):
+        for old in (CALLS_FOR, CALLS):   # not to be taken for the new one if that fails
+            if os.path.exists(old):
+                os.remove(old)
         base = os.path.dirname(torch.__file__)
         inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
                os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -83,6 +97,8 @@ def build_calls(force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"{CXX} failed on {src}:\n{r.stdout}\n{r.stderr}")
         os.replace(CALLS + ".tmp", CALLS)
+        with open(CALLS_FOR, "w") as f:
+            f.write(wanted)
     return CALLS
 
 
