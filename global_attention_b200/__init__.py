@@ -815,7 +815,8 @@ def _kv8(cache):
 def zgcm_kv8_append(cache, k, v, pos, *, count=None, stream=None):
     """Append tokens: k (cache.key_dtype, prepared: zgcm_qk_norm_rope_fwd) and v (bf16) [n_seq, N, Hkv, D], rows
     contiguous, other strides multiples of 8; pos int32 [n_seq], the first token's position (negative: the sequence
-    is idle); count int32 [n_seq], the tokens of each sequence (default N).  Updates the cache in place."""
+    is idle); count int32 [n_seq], the tokens of each sequence (default N).  Updates the cache in place.  A sequence may be
+    rewound to a position of its newest block or to a multiple of 64 before it, not into an earlier block."""
     _done(_quick().kv8_append(*_kv8(cache), k, v, pos, count, stream), "zgcm_kv8_append")
     return cache
 

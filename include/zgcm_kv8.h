@@ -69,6 +69,14 @@ typedef struct {
  * read.  Blocks that the call completes are coded, except those that the ring overwrites
  * within the same call; the newest block is written to the tail, whose rows past the newest
  * token keep what they hold.  A block whose page number is bad is not stored.
+ *
+ * Rewinding (a rejected draft, an answer given anew): pos[b] may be any position of the block of
+ * the last token appended, or the first position (a multiple of 64) of an earlier block; the
+ * tokens from there on are then those of this call.  Not a position inside an earlier block: that
+ * block's first tokens would be taken from the tail, which has held a later block since, and the
+ * call cannot know; append it from its first position.  A ring that has stored later blocks has lost
+ * those that they replaced: a sequence can go back by as many blocks as n_blocks exceeds the
+ * ceil((window-1)/64) + 1 that its window touches.
  */
 int zgcm_kv8_append(const zgcm_kv8_cache* cache, const void* k, long long k_b_stride, long long k_t_stride,
                     long long k_h_stride, const void* v, long long v_b_stride, long long v_t_stride,

@@ -11,7 +11,7 @@ import torch
 
 import global_attention_b200 as ga
 from oracle import kv8
-from test_kv8 import ALL, KEY, _feed, _i32, _means, _new, _queries, _tokens, cuda  # noqa: F401  (cuda: the fixture)
+from test_kv8 import ALL, KEY, _check_decode, _feed, _i32, _means, _new, _queries, _tokens, cuda  # noqa: F401  (cuda: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -141,3 +141,21 @@ def test_slices_of_positions_and_lists(cuda):  # noqa: F811
                 assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(held, alone))
             steps[2] = _i32(299, 280, 299)
     assert all(torch.equal(x, y) for x, y in zip(*kept))
+
+
+@gpu
+@pytest.mark.parametrize("n_blocks,window", [(6, ALL), (5, 130)])
+def test_rewinding(cuda, n_blocks, window):  # noqa: F811
+    """Back to a position of the newest block, and to the first position of earlier ones, other tokens from there on: the cache
+    and the attention are those of the sequence as it is then.  (A table of 5 blocks is one more than a window of 130
+    touches: it goes back by one.)"""
+    k, v = _tokens(2, 330, 2, "bf16", seed=33)
+    others = _tokens(2, 330, 2, "bf16", seed=34)
+    c = _new(2, n_blocks, 2, "e4m3", "bf16")
+    _feed(c, k[:, :270], v[:, :270], [70, 199, 1])
+    q, g = _queries(2, 4, "bf16")
+    # 270 tokens -> 257 .. 275 (newest block 4), 256 .. 260 (its first position), 192 .. 240 (a block earlier), 200 .. 310
+    for start, end in ((257, 275), (256, 260), (192, 240), (200, 310)):
+        k[:, start:end], v[:, start:end] = others[0][:, start:end], others[1][:, start:end]
+        _feed(c, k[:, start:end], v[:, start:end], [end - start], start=start)
+        _check_decode(c, k[:, :end], v[:, :end], q, g, "e4m3", window=window)
