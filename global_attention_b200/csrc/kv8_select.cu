@@ -332,10 +332,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
             for (int i = i0 + tid; i < i1; i += THREADS) atomicAdd(&hist[step(score[i])], 1u);
             __syncthreads();
             find_step<THREADS>(sm, hist, need);
-            // the step's edges (its own rounding is 2^-12 of a step, theirs less than 2^-22 of a score: within eps)
+            // The step's edges.  Four roundings of 2^-24 in a score's place among the SEL_BINS steps and four in an edge's:
+            // 2^-21 SEL_BINS of a step together; adding lo is 2^-24 of a score, within the room that eps has.
+            constexpr float off = SEL_BINS * 0x1p-21f;
             const float eps = 0x1.7p-15f * __uint_as_float(sm.q1) * magnitude<TK>(sm.mean_max) + 0x1p-100f;
-            const float v0 = lo + ((float)sm.bin - 0x1p-11f) * (width / (SEL_BINS - 1)) - 2.f * eps;
-            const float v1 = lo + ((float)sm.bin + (1.f + 0x1p-11f)) * (width / (SEL_BINS - 1)) + 2.f * eps;
+            const float v0 = lo + ((float)sm.bin - off) * (width / (SEL_BINS - 1)) - 2.f * eps;
+            const float v1 = lo + ((float)sm.bin + (1.f + off)) * (width / (SEL_BINS - 1)) + 2.f * eps;
             // taken, not taken, and the list of those between
             uint32_t above = 0;
             for (int i = i0 + tid; i < i1; i += THREADS) {
