@@ -11,7 +11,8 @@ import torch
 
 import global_attention_b200 as ga
 from oracle import kv8
-from test_kv8 import ALL, KEY, _check_decode, _feed, _i32, _means, _new, _queries, _tokens, cuda  # noqa: F401  (cuda: the fixture)
+from test_kv8 import (ALL, KEY, _check_decode, _check_select, _feed, _i32, _means, _new, _queries, _tokens,  # noqa: F401
+                      cuda)  # (the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -159,3 +160,42 @@ def test_rewinding(cuda, n_blocks, window):  # noqa: F811
         k[:, start:end], v[:, start:end] = others[0][:, start:end], others[1][:, start:end]
         _feed(c, k[:, start:end], v[:, start:end], [end - start], start=start)
         _check_decode(c, k[:, :end], v[:, :end], q, g, "e4m3", window=window)
+
+
+@gpu
+@pytest.mark.parametrize("key", ["bf16", "fp16"])
+@pytest.mark.parametrize("blocks,near", [(700, 200), (700, 500), (2500, 256), (2500, 1000)])
+@pytest.mark.parametrize("G", [1, 12])
+def test_select_by_less_than_a_rounding(cuda, key, blocks, near, G):  # noqa: F811
+    """`near` blocks whose scores are 2^15 - 2^15 + i 2^-20, which fp32 sums cannot tell apart, the cut in their middle: as
+    few as are ranked one by one (256 at most) and more; one of G heads has these scores, the others' are lower."""
+    gen = torch.Generator().manual_seed(blocks + near)
+    c = _new(1, blocks, 1, "e4m3", key, garbage=False)
+    at = torch.randperm(blocks - 1, generator=gen)
+    mean = torch.zeros(blocks, 128)
+    mean[:, :2] = 2.0 ** 15
+    i = torch.arange(near)
+    mean[at[:near], 2], mean[at[:near], 3] = (i >> 6) * 2.0 ** -6, (i & 63) * 2.0 ** -6
+    mean[at[near:near + 100], 4], mean[at[near + 100:], 4] = 64.0, -64.0
+    mean[:, 5] = 1000.0
+    c.k_mean[c.table[0].long(), 0] = mean.to(KEY[key]).cuda()
+    q = torch.zeros(1, G, 128)
+    q[0, :, 5] = -1.0
+    q[0, -1, :6] = torch.tensor([1.0, -1.0, 2.0 ** -8, 2.0 ** -14, 1.0, 0.0])
+    assert (np.float32(2 ** 15) + (i * 2.0 ** -20).float().numpy() == np.float32(2 ** 15)).all()
+    got = _check_select(c, q.to(KEY[key]), [64 * blocks], 100 + near // 2, 0, 0)
+    # by hand: the 100 above and the upper half of the near ones
+    assert sorted(at[near // 2 + near % 2:near + 100].tolist()) == got[0, 0].tolist()
+
+
+@gpu
+@pytest.mark.parametrize("key", ["bf16", "fp16"])
+@pytest.mark.parametrize("blocks", [2048, 5000])
+def test_select_of_many_heads_and_blocks(cuda, key, blocks):  # noqa: F811
+    """More heads than one round of the scores takes, and more blocks than one CTA does."""
+    c = _new(1, blocks, 2, "e4m3", key, garbage=False)
+    _means(c, seed=blocks)
+    for Hq in (18, 24, 34):
+        q, _ = _queries(1, Hq, key, seed=Hq)
+        for n, first, last in ((3, 0, 0), (64, 1, 1), (700, 2, 3)):
+            _check_select(c, q, [64 * blocks], n, first, last)
