@@ -31,8 +31,12 @@ __device__ __forceinline__ int kv8_page(const Kv8& c, int b, int j) {
     return (unsigned)p < (unsigned)c.P ? p : -1;
 }
 
-__device__ __forceinline__ float key_to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float key_to_float(bf16 x) { return __bfloat162float(x); }
+// the value of a 16-bit type's bits
+template <typename T> __device__ __forceinline__ float from_bits(uint32_t b);
+template <> __device__ __forceinline__ float from_bits<bf16>(uint32_t b) { return __uint_as_float(b << 16); }
+template <> __device__ __forceinline__ float from_bits<__half>(uint32_t b) {
+    return __half2float(__ushort_as_half((unsigned short)b));
+}
 
 // checks of a cache; ZGCM_OK with *out filled
 int kv8_check(const zgcm_kv8_cache* c, Kv8* out);

@@ -69,11 +69,6 @@ template <> __device__ __forceinline__ float2 unpack2<bf16>(uint32_t u) { return
 template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
-template <typename T> __device__ __forceinline__ float from_bits(uint32_t b);
-template <> __device__ __forceinline__ float from_bits<bf16>(uint32_t b) { return __uint_as_float(b << 16); }
-template <> __device__ __forceinline__ float from_bits<__half>(uint32_t b) {
-    return __half2float(__ushort_as_half((unsigned short)b));
-}
 
 // Two quotients x / s, correctly rounded: r = 1 / s rounded to nearest; x r is off by less than two units in the last
 // place, one step with the exact remainder x - q s brings it within one, and from there a second one gives the

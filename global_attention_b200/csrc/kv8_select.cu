@@ -55,13 +55,6 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(uint32_t k) { return __uint_as_float((int)k < 0 ? k & 0x7fffffffu : ~k); }
 
-// the value of a 16-bit type's magnitude bits
-template <typename T> __device__ __forceinline__ float magnitude(uint32_t bits);
-template <> __device__ __forceinline__ float magnitude<bf16>(uint32_t bits) { return __uint_as_float(bits << 16); }
-template <> __device__ __forceinline__ float magnitude<__half>(uint32_t bits) {
-    return __half2float(__ushort_as_half((unsigned short)bits));
-}
-
 // exclusive scan over the CTA; every thread calls it
 template <int WARPS> __device__ __forceinline__ uint32_t cta_scan(uint32_t x, uint32_t* red) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -335,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_select_kernel(con
             // The step's edges.  Four roundings of 2^-24 in a score's place among the SEL_BINS steps and four in an edge's:
             // 2^-21 SEL_BINS of a step together; adding lo is 2^-24 of a score, within the room that eps has.
             constexpr float off = SEL_BINS * 0x1p-21f;
-            const float eps = 0x1.7p-15f * __uint_as_float(sm.q1) * magnitude<TK>(sm.mean_max) + 0x1p-100f;
+            const float eps = 0x1.7p-15f * __uint_as_float(sm.q1) * from_bits<TK>(sm.mean_max) + 0x1p-100f;
             const float v0 = lo + ((float)sm.bin - off) * (width / (SEL_BINS - 1)) - 2.f * eps;
             const float v1 = lo + ((float)sm.bin + (1.f + off)) * (width / (SEL_BINS - 1)) + 2.f * eps;
             // taken, not taken, and the list of those between
