@@ -26,6 +26,7 @@
  * Arithmetic is fp32 (angles are formed and reduced in fp64); each output element is
  * rounded once.  The sums of dgamma run in a fixed order: results repeat bit for bit.
  * A non-finite x makes its own row non-finite and no other.
+ * The sum of a row's squares has to stay within fp32 (elements below 2^60), and above its smallest numbers where eps is 0.
  * Shapes: D == 128; Hq, Hkv >= 1; rope_dims even, 0 .. 128; T >= 0 (0: nothing is computed,
  * the backward zeroes dgamma_q and dgamma_k).
  * Errors and streams as in zgcm_attn.h: checks before any launch, asynchronous on
