@@ -212,18 +212,21 @@ template <typename TK, int CODE> cudaError_t launch(const DecodeKv8Params& p, cu
 // Whether this kernel takes the call, and how an item is split.  units: the most an item can have.
 //
 // An item is split while there are CTA places left on the 148 SMs (two CTAs an SM) and a CTA keeps more than one unit; the
-// kernel takes the call while a CTA has at most 64 units, or 32 where the CTAs do not fill the SMs, which the equal runs
-// of kv8_decode_kernel do whatever the items.  Measured (us; 8 KV heads of 4, int8, this kernel / that one):
-//   1 sequence of     1000 7.6 / 12.8, 16K 20.7 / 29.6, 32K (31 units a CTA) 32.7 / 36.5, 64K with 8 CTAs an item 96 / 50
-//   16 sequences of   8K (63 units a CTA) 60 / 65, 16K 113 / 108
-//   64 of up to       4K (65) 81 / 87, 8K 156 / 154, 16K 299 / 280: lengths differ, and the longest item decides
+// kernel takes the call while a CTA has at most 64 units (48 where groups have more than 4 heads), or 32 where the CTAs do not
+// fill the SMs, which the equal runs of kv8_decode_kernel do whatever the items.  Measured (us; int8, this kernel / that one;
+// "to": lengths of half that and more, where the longest item decides):
+//   8 KV heads of 4, 1 sequence of 1000 7.6 / 12.8, 16K 21.3 / 30.4, 32K (31 units a CTA) 33.2 / 37.4, 64K 60 / 51
+//   16 sequences of   8K (64) 61 / 70, to 8K 57 / 55, to 16K 107 / 88
+//   64 to             4K (64) 82 / 88, 8K 155 / 153, 16K 315 / 291
+//   4 KV heads of 8, 1 of 32K (31) 38 / 44, 64K 63 / 49;  16 to 8K (32) 38 / 39, 12K (47) 52 / 46, 16K (64) 69 / 55
+//   64 of 3000 (47) 55 / 60, to 3000 53 / 50, of 4K (64) 70 / 71, to 4K 69 / 57
 // and 16 CTAs an item against 8: 1 x 4K 10.8 / 12.3, 1 x 16K 20.7 / 29.4; two CTAs an SM against four: 4 x 16K 35 / 47,
 // 32 listed blocks of 16 sequences 24.9 / 25.2.
 bool kv8_direct_plan(DecodeKv8Params& p, int units) {
     const long long items = (long long)p.c.B * p.c.Hkv * p.HT;
     p.split = 1;
     while (p.split < DD_SPLIT && items * p.split * 2 <= 296 && units > 2 * p.split) p.split *= 2;
-    return units <= (items * p.split >= 148 ? 64 : 32) * p.split;
+    return units <= (items * p.split < 148 ? 32 : p.G > DK_HEADS / 2 ? 48 : 64) * p.split;
 }
 
 cudaError_t kv8_direct_launch(const DecodeKv8Params& p, cudaStream_t stream) {
