@@ -8,8 +8,9 @@
 //
 // Bound by HBM for prompts (2 bytes read, 1 written per value) and by latency for single
 // tokens, which move one row per head and, every 64th token, a block.
-// Measured on a B200: prompts of up to 16K for 4 sequences (303 MB) 54.5 us, 5.6 TB/s, 86% of the measured copy rate, with
-// four CTAs an SM (64 registers); one token each for 64 sequences 4.2 us.
+// Measured on a B200 in a graph's replays: prompts of up to 16K for 4 sequences (303 MB) 54.5 to 57.5 us on different cards, 5.6
+// to 5.3 TB/s, 82 to 86% of the measured copy rate, with four CTAs an SM (64 registers); as eager calls on cold inputs 54 to
+// 65 us; one token each for 64 sequences 4.8 us.
 #include "kv8.cuh"
 #include "sm100.cuh"
 

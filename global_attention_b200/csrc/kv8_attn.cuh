@@ -164,7 +164,8 @@ __device__ __forceinline__ float quad_max(float x) {
 // than 4 heads in a group) multiply twice.  Others have the columns 4 .. 7 free: they hold the four heads again, the same
 // scores, maxima and sums, but take the low halves, and O's two columns of a head are added at the item's end: no
 // product more than with one half.  Measured with one half / with both (us): 64 sequences of up to 16K, INT8, 8 KV heads of 4
-// 273 / 280, 4 of 8 158 / 152, 2 of 16 137 / 143; 64 of up to 8K, one of 12 59 / 72; 32 listed blocks 24.6 / 24.6.
+// 273 / 280, 4 of 8 158 / 152, 2 of 16 137 / 143; 16 of up to 8K, 4 of 8 33 / 38; 32 listed blocks 24.6 / 24.6, 4 of 8
+// 16.7 / 19.4.
 struct State {
     float2 m, l;      // running maximum (base 2), this lane's part of the sum (times 2^14)
     float2 o[8][2];

@@ -9,8 +9,9 @@
 // to shared memory, and its 128 rows would be heads, 4 of them real, or its smallest N twice these):
 //   S^T = K Q^T: 16 keys x 16 dims of codes by q of the heads;
 //   O^T = V^T P: 16 dims x 16 keys of codes by p, which is S^T's result transposed in registers (movmatrix).
-// A block takes 1350 instructions of a warp as E4M3, 1530 as INT8, for 4 heads.  (Heads as rows, zero-filled to 16, with
-// p in two halves in the idle rows, took 1750: the multiplier's four-register operand was half zeros.)
+// p enters in two fp16 halves (kv8_attn.cuh says how, at State).
+// A block takes 1360 instructions of a warp as E4M3, 1560 as INT8, for up to 4 heads, 1700 as INT8 for up to 8.  (Heads as
+// rows, zero-filled to 16, with p in two halves in the idle rows, took 1750: the multiplier's four-register operand was half zeros.)
 // Codes become fp16 exactly and their scales multiply the fp32 sums, once per block: the scores by
 // ks, the block's O by vs where it joins the running O.  E4M3 pairs are converted by one instruction;
 // an INT8 code x as the byte x + 128 under the exponent of 1024, less 1152 (taking the 128 off the
@@ -26,9 +27,10 @@
 // there, pieces of a cut one go to the workspace and kv8_join_kernel finishes them (launched early, by
 // programmatic dependent launch).  Results depend on positions and shapes alone.
 // Calls whose items have few blocks go to kv8_direct.cu, which says at kv8_direct_plan where the border is and why.
-// Measured on a B200 (6.47 TB/s as a copy): 64 sequences of 8K to 16K, 8 KV heads of 4, INT8: 275 us for 1.62 GB, 5.9 TB/s,
-// 91% of the copy rate (313 us with two CTAs an SM).  One sequence of 64K: 49 us, where the bytes take 21: some 20 us are the
-// start, the cut items' records and the join.
+// Measured on a B200 (6.47 TB/s as a copy): 64 sequences of 8K to 16K, 8 KV heads of 4, INT8, 1.62 GB: 282 to 285 us in a
+// graph's replays, 5.7 TB/s, 88% of the copy rate, 279 to 300 as eager calls on different cards (a seventh more with two
+// CTAs an SM).  One sequence of 64K: 51 us, where the bytes take 21: some 20 us are the start, the cut items' records and the
+// join.
 #include <cudaTypedefs.h>
 #include <math.h>
 

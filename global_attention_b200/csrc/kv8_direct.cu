@@ -7,8 +7,8 @@
 // decides a CTA's work, the rows of q and of the tail load while page numbers do, the CTAs' parts meet in
 // shared memory across the cluster (each is sent its share of all, and finishes it), and there is no second kernel.  Four CTAs of
 // four warps fit on an SM: their latencies overlap.
-// Measured on a B200, 8 KV heads of 4: one sequence of 1000 tokens 7.3 us (an empty call takes 2); a window of 128 for 64
-// sequences 10.7 us, 23 MB; 32 selected blocks for 16 sequences 22.8 us, 70 MB, 3.1 TB/s: position, table, list, page and
+// Measured on a B200 in a graph's replays, 8 KV heads of 4: one sequence of 1000 tokens 7.6 us (an empty call takes 2); a
+// window of 128 for 64 sequences 10.8 us, 23 MB; 32 selected blocks for 16 sequences 23.2 us, 70 MB, 3.0 TB/s: position, table, list, page and
 // codes follow each other, 0.6 to 1 us each from HBM, and 256 CTAs' copies are not many enough to fill that time.
 #include <cooperative_groups.h>
 

@@ -6,8 +6,9 @@
 //
 // Bound by HBM: forward reads x and writes y, backward reads x and dy and writes dx, and no
 // value is used twice except by its own row.  What has to stay small beside it is the number of
-// instructions: at the rate of HBM an SM has 88 issue slots for a row forward.  Measured on a B200, 32 + 8 heads, bf16: 65536
-// tokens forward 224 us, 6.0 TB/s (93% of a copy's rate), backward 346 us, 5.8 TB/s; 64 tokens 3.1 us, 1000 backward 11.3 us.
+// instructions: at the rate of HBM an SM has 88 issue slots for a row forward.  Measured on a B200 in a graph's replays, 32 + 8
+// heads, bf16: 65536 tokens forward 223 us, 6.0 TB/s (93% of a copy's rate), backward 352 us, 5.7 TB/s; 64 tokens 3.1 us, 1000
+// backward 12.0 us.
 // So a row of
 // 128 belongs to 8 lanes, 16 elements each in two chunks (8 l .. and 64 + 8 l .., one 16-byte
 // access of a 16-bit type each): a warp works on 4 rows at once, their sums are 3 shuffles, and
