@@ -95,7 +95,7 @@ int zgcm_kv8_append(const zgcm_kv8_cache* cache, const void* k, long long k_b_st
  * mean); out bf16 [n_seq, Hq, D]; lse fp32 [n_seq, Hq].  Idle sequences: out 0, lse -inf.
  * A window that reaches further back than n_blocks blocks (the own one among them): NaN.
  * Probabilities enter their products with 22 bits or more; scores, sums and out are fp32 and out is rounded once.  A value of the
- * own block that is not finite makes out NaN in its dim.  v_scale times 2^-14 is fp32: blocks of values below 2^-103 lose bits.
+ * own block that is not finite makes out not finite in its dim.  v_scale times 2^-14 is fp32: blocks of values below 2^-103 lose bits.
  * workspace: zgcm_attn_decode_kv8_workspace_size bytes (n_list < 0: no list), 16-byte aligned, contents on
  * entry irrelevant, not used by a concurrent call.  0, and workspace may be NULL, where no sequence can have many blocks to
  * read, and for arguments that zgcm_attn_decode_kv8 rejects; positions do not matter.

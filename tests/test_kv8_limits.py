@@ -199,3 +199,49 @@ def test_select_of_many_heads_and_blocks(cuda, key, blocks):  # noqa: F811
         q, _ = _queries(1, Hq, key, seed=Hq)
         for n, first, last in ((3, 0, 0), (64, 1, 1), (700, 2, 3)):
             _check_select(c, q, [64 * blocks], n, first, last)
+
+
+@gpu
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (12, 2)])
+@pytest.mark.parametrize("S", [40, 200, 33000])
+def test_non_finite_values_of_the_newest_block(cuda, Hq, Hkv, S):  # noqa: F811
+    """An infinity or NaN among the values in 16 bits: out is not finite in its dim, for the heads that read it, and as ever
+    elsewhere; out of the window, or behind the newest token, it does not matter."""
+    k, v = _tokens(1, S, Hkv, "bf16", seed=S)
+    q, g = _queries(1, Hq, "bf16")
+    clean = v.clone()
+    v[0, S - 5, 0, 7], v[0, S - 2, 0, 100], v[0, S - 3, 1, 50] = float("inf"), float("nan"), float("-inf")
+    c = _new(1, S // 64 + 1, Hkv, "e4m3", "bf16")
+    _feed(c, k, v, [S])
+    same = _new(1, S // 64 + 1, Hkv, "e4m3", "bf16")
+    _feed(same, k, clean, [S])
+    args = q.cuda(), g.cuda(), _i32(S - 1)
+    out, lse = ga.zgcm_attn_decode_kv8(c, *args, window=ALL)
+    ref, ref_lse = ga.zgcm_attn_decode_kv8(same, *args, window=ALL)
+    bad = torch.zeros(1, Hq, 128, dtype=torch.bool, device="cuda")
+    bad[:, :Hq // 2, 7] = bad[:, :Hq // 2, 100] = bad[:, Hq // 2:, 50] = True
+    assert torch.equal(torch.isfinite(out), ~bad) and torch.equal(out[~bad], ref[~bad]) and torch.equal(lse, ref_lse)
+    out, lse = ga.zgcm_attn_decode_kv8(c, *args, window=1)
+    ref, ref_lse = ga.zgcm_attn_decode_kv8(same, *args, window=1)
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@gpu
+def test_slices_on_another_stream(cuda):  # noqa: F811
+    """A slice of positions is copied on the call's stream, behind what that stream writes into it."""
+    k, v = _tokens(3, 6400, 2, "bf16", seed=35)
+    q, g = (x.cuda() for x in _queries(3, 4, "bf16"))
+    c = _new(3, 100, 2, "int8", "bf16")
+    _feed(c, k, v, [6400])
+    ref = ga.zgcm_attn_decode_kv8(c, q, g, _i32(6399, 6399, 6399), window=ALL)
+    steps, side = _i32(*[-1] * 7), torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            busy = busy @ busy * 1e-3
+        steps.fill_(6399)
+    out = ga.zgcm_attn_decode_kv8(c, q, g, steps[3:6], window=ALL, stream=side)
+    sel = ga.zgcm_kv8_select(c, q, steps[3:6], 5, window=ALL, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, ref)) and (sel >= 0).all()
